@@ -112,9 +112,9 @@ def prepare(case, seed):
 
 
 def _eight_bits(x):
-    """Rows of 8-bit integers and their scales: scale = max |x| / 127 in 32 bits, value = x / scale to the nearest
-    integer, halves to the even one (in 64 bits, where no quotient near a half is lost)."""
-    scale = x.float().abs().amax(1) / 127.0
+    """Rows of 8-bit integers and their scales: scale = max |x| / 127 rounded to 32 bits, value = x / scale to the
+    nearest integer, halves to the even one (quotients in 64 bits: those near a border are not lost)."""
+    scale = (x.double().abs().amax(1) / 127.0).float()
     q = (x.double() / scale.double()[:, None]).round()
     return torch.where(scale[:, None] > 0, q, torch.zeros_like(q)), scale
 
@@ -228,7 +228,7 @@ def exact(case, seed):
     e, c = (s[name].detach().double() for name in ("e", "c"))
     bias = None if s["bias"] is None else s["bias"].detach().double()
     if "scale" in s:
-        step = (s["e"].abs().amax(1).float() / 127.0).double()[:, None]
+        step = (s["e"].double().abs().amax(1) / 127.0).float().double()[:, None]
         e = torch.where(step > 0, torch.round(e / step), 0.0) * step
         c *= s["scale"].double()[:, None]
     leaves = [t.requires_grad_(op == "train") for t in (e, c, bias) if t is not None]
