@@ -86,7 +86,8 @@ def prepare(case, seed):
 
     c = normal(v, d).mul_(d ** -0.5)
     best = torch.randint(0, v, (n,), generator=g, device=dev)
-    e = (normal(n, d) + 11.0 * c[best]).to(torch.bfloat16)
+    t = case.get("temperature", 1.0)  # the other logits are about normal: their exp(z / t) add up to v exp(1 / 2 t^2)
+    e = (normal(n, d) + t * (math.log(v / 2) + 0.5 / t ** 2) * c[best]).to(torch.bfloat16)
     s = dict(case=case, e=e)
     if op == "int8" or case.get("int8"):
         s["scale"] = c.abs().amax(1).div_(127.0)
