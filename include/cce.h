@@ -246,6 +246,90 @@ CCE_API cce_status cce_forward_noalloc(const cce_problem* p, const void* E, cons
                                        const int64_t* targets, float* loss, float* lse, float* tile_max,
                                        int64_t* count, cce_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Log-probabilities of given tokens, entropy and top alternatives of a classifier head, without the
+ * [N, V] logits in memory; and the product with a classifier of 8-bit integers. The pages have no
+ * counterpart beyond the log-sum-exp they share with the loss.
+ *
+ * With z = E C^T + bias, y = z / temperature, p = softmax(y), lse = ln sum_v exp(y_v), per row:
+ *   log-probability of a given token t: y_t - lse;   entropy: lse - sum_v p_v y_v;
+ *   alternatives: the top_k tokens with the largest y, highest first, the lower id first among equal
+ *   ones, with y - lse. Close alternatives are ordered by their logits in 64 bits.
+ * A given token equal to ignore_index asks for nothing: its log-probability is 0; a row of which every
+ * token is has entropy 0 and gradient 0, whatever stands in its row of E. A token outside [0, V) gives
+ * NaN in its place, and CCE_ERR_TARGET_RANGE from cce_check_device_error(). A bias of -inf takes a
+ * column out of the softmax; a row of which nothing is left has log-probabilities -inf, entropy 0 and
+ * gradient 0.
+ *
+ * 8-bit operands: a row x is held as integers q and one scale, x ~ q * scale, scale = max |x| / 127
+ * rounded to fp32 and q = x / scale rounded to the nearest integer (the even one of two). The
+ * classifier is given so (int8 [V, D], scales fp32 [V]; cce_quantize_int8 makes it); E is bf16 and is
+ * rounded to 8 bits row by row inside the call. z = (sum_d qe qc) se sc + bias, the sum exact.
+ * D is then a multiple of 16, at most 131072.
+ */
+typedef struct {
+  int64_t N;            /* rows of E, >= 0 */
+  int64_t D;            /* hidden size; multiple of 8 (16 with int8) */
+  int64_t V;            /* rows of C, >= 1 */
+  int64_t ignore_index; /* a given token equal to this asks for nothing */
+  int32_t num_tokens;   /* given tokens a row, 0 to 32 */
+  int32_t top_k;        /* alternatives a row, 0 to 24, at most V */
+  float temperature;    /* > 0 */
+  int32_t int8;         /* 1: C is int8 with the scales c_scale; 0: C is bf16 */
+  int32_t reserved;     /* must be 0 */
+} cce_logprob_problem;
+
+/* Bytes of device workspace cce_logprobs() needs (0 for a bad problem). Of the order of N * 12 bytes a
+ * segment (a row block's share of one SM, 2 * (148 / row blocks + 1) of them), 24 times that with
+ * alternatives, and with int8 E once more: never anything of size N * V. */
+CCE_API size_t cce_logprobs_workspace_size(const cce_logprob_problem* p);
+
+/*
+ *  E        device bf16 [N, D]
+ *  C        device bf16 [V, D], or int8 [V, D] (p->int8) with c_scale device fp32 [V] (else NULL)
+ *  bias     device bf16 [V] or NULL
+ *  tokens   device int64 [N, num_tokens] (NULL when num_tokens is 0)
+ *  logprobs device fp32 [N, num_tokens], entropy fp32 [N], lse fp32 [N] (num_tokens > 0)
+ *  tile_max device fp32 [ceil(V / 64) * N] or NULL: saved for a backward with filter_eps > 0
+ *  top_logprobs device fp32 [N, top_k], top_ids int64 [N, top_k] (top_k > 0)
+ * After a device error (a bounded wait that ran out) every output is NaN, and every id -1.
+ */
+CCE_API cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void* C, const float* c_scale,
+                                const void* bias, const int64_t* tokens, float* logprobs, float* entropy, float* lse,
+                                float* tile_max, float* top_logprobs, int64_t* top_ids, void* workspace,
+                                size_t workspace_bytes, cce_stream_t stream);
+
+/* Bytes of device workspace cce_logprobs_backward() needs (0 for a bad problem): that of
+ * cce_backward(), a copy of E, and 16 + 8 num_tokens bytes a row. */
+CCE_API size_t cce_logprobs_backward_workspace_size(const cce_logprob_problem* p, int32_t out_fp32);
+
+/*
+ * Gradients of sum_k g_k logprob_k + h entropy for E, C and bias, with grad_logprobs g device fp32
+ * [N, num_tokens] and grad_entropy h device fp32 [N] (either may be NULL: zeros):
+ *   dz_v = (sum_k g_k [v = t_k] - p_v (sum_k g_k + h (ln p_v + entropy))) / temperature.
+ * lse and entropy as cce_logprobs() returned them. filter_eps > 0 skips units of 128 rows x 64 columns
+ * as cce_backward() does, except those that hold a given token (tile_max is then needed); 0 keeps all.
+ * dE, dC, dbias, out_fp32 and filtered_tiles as for cce_backward().
+ */
+CCE_API cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, const void* C, const void* bias,
+                                         const int64_t* tokens, const float* lse, const float* entropy,
+                                         const float* tile_max, const float* grad_logprobs, const float* grad_entropy,
+                                         float filter_eps, void* dE, void* dC, void* dbias, int32_t out_fp32,
+                                         int64_t* filtered_tiles, void* workspace, size_t workspace_bytes,
+                                         cce_stream_t stream);
+
+/* Rows of x (device bf16 [rows, D]) as 8-bit integers q [rows, D] and scales fp32 [rows]. A row of
+ * zeros gets scale 0; a row with an infinity or a NaN gets the scale NaN. */
+CCE_API cce_status cce_quantize_int8(const void* x, int64_t rows, int64_t D, int8_t* q, float* scale,
+                                     cce_stream_t stream);
+
+/* The logits z themselves, out device [N, V] in bf16 (out_fp32 = 0) or fp32 (1), for a classifier of
+ * 8-bit integers. The workspace holds E in 8 bits. */
+CCE_API size_t cce_int8_linear_workspace_size(int64_t N, int64_t D, int64_t V);
+CCE_API cce_status cce_int8_linear(int64_t N, int64_t D, int64_t V, const void* E, const int8_t* C,
+                                   const float* c_scale, const void* bias, void* out, int32_t out_fp32,
+                                   void* workspace, size_t workspace_bytes, cce_stream_t stream);
+
 /* Optional instrumentation, off by default and per calling thread. When an event pair is set
  * (cudaEvent_t handles created by the caller; NULL clears), cce_forward() records fwd_start and
  * fwd_stop on its stream immediately before and after launching its tensor-core kernel, and

@@ -13,18 +13,35 @@
 #include <string>
 
 #include "cce.h"
+#include "cce_host.h"
 #include "cce_internal.h"
 
 namespace {
 
-constexpr int32_t kVersion = 500;  // 0.5.0: the skip rule on 128 x 64 units (saved maxima per 64 columns)
-constexpr size_t kHeaderBytes = 256;
-constexpr size_t kAlign = 256;
+constexpr int32_t kVersion = 600;  // 0.6.0: log-probabilities, top alternatives, 8-bit product
+
+using cce::aligned16;
+using cce::align_up;
+using cce::ceil_div;
+using cce::check_device;
+using cce::cuda_fail;
+using cce::fail;
+using cce::get_encoder;
+using cce::kHeaderBytes;
+using cce::make_map;
+using cce::WsHeader;
 
 thread_local std::string g_last_error;
 thread_local int64_t g_launches = 0;
 thread_local cudaEvent_t g_fwd_ev[2] = {nullptr, nullptr};
 thread_local cudaEvent_t g_bwd_ev[2] = {nullptr, nullptr};
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+}  // namespace
+
+namespace cce {
 
 cce_status fail(cce_status s, const char* fmt, ...) {
   char buf[512];
@@ -40,16 +57,52 @@ cce_status cuda_fail(cudaError_t e, const char* what) {
   return fail(CCE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Layout of the area at the start of every workspace (zeroed by every call).
-struct WsHeader {
-  int err;   // device error word
-  int done;  // blocks of the forward's finish kernel that are done
-  int bar;   // grid barrier counter of the backward's planning launch
-};
+void clear_last_error() { g_last_error.clear(); }
 
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+cce_status get_encoder() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (g_encode == nullptr) return fail(CCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  return CCE_OK;
+}
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+cce_status check_device(int* num_sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  int major = 0, minor = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major != 10 || minor != 0)
+    return fail(CCE_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a (B200)", dev, major,
+                minor);
+  e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  return CCE_OK;
+}
+
+// 2-D row-major tensor [rows, cols] with contiguous rows, box [box_rows, box_cols], 128B swizzle.
+cce_status make_map(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem, const void* ptr, int64_t rows,
+                    int64_t cols, uint32_t box_cols, uint32_t box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = g_encode(map, dtype, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CCE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return CCE_OK;
+}
+
+}  // namespace cce
+
+namespace {
 
 // Size of the whole vocabulary: the classifier's rows, or vocab_total for a shard of it.
 int64_t vocab_total(const cce_problem* p) { return p->vocab_total > 0 ? p->vocab_total : p->V; }
@@ -241,77 +294,49 @@ SplitWs carve_split(const cce_problem* p, int32_t out_fp32, void* base) {
   return w;
 }
 
-bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+// What the backward of the log-probabilities keeps behind the loss's workspace (cce_aux.cu: logprob_prep_kernel).
+struct LogprobWs {
+  cce::LogprobPrep prep;
+  size_t bytes;  // with the SplitWs before it
+};
 
-// ---------------------------------------------------------------------------------------------
-// Device checks and TMA descriptors
-// ---------------------------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-cce_status get_encoder() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (g_encode == nullptr) return fail(CCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  return CCE_OK;
+LogprobWs carve_logprob(const cce_problem* p, int K, size_t off, void* base) {
+  LogprobWs w{};
+  char* b = static_cast<char*>(base);
+  auto take = [&](size_t bytes) {
+    char* ptr = b + off;
+    off = align_up(off + bytes);
+    return ptr;
+  };
+  const size_t n = static_cast<size_t>(p->N), k = static_cast<size_t>(K);
+  w.prep.coef = reinterpret_cast<float*>(take(sizeof(float) * n));
+  w.prep.coef_log = reinterpret_cast<float*>(take(sizeof(float) * n));
+  w.prep.lse = reinterpret_cast<float*>(take(sizeof(float) * n));
+  w.prep.tok = reinterpret_cast<int*>(take(sizeof(int) * n * k));
+  w.prep.tok_g = reinterpret_cast<float*>(take(sizeof(float) * n * k));
+  w.prep.targets = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * n));
+  w.prep.one = reinterpret_cast<float*>(take(sizeof(float)));
+  w.prep.E_out = reinterpret_cast<__nv_bfloat16*>(take(2 * n * static_cast<size_t>(p->D)));
+  w.bytes = off;
+  return w;
 }
-
-cce_status check_device(int* num_sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 0)
-    return fail(CCE_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a (B200)", dev, major,
-                minor);
-  e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  return CCE_OK;
-}
-
-// 2-D row-major tensor [rows, cols] with contiguous rows, box [box_rows, box_cols], 128B swizzle.
-cce_status make_map(CUtensorMap* map, CUtensorMapDataType dtype, size_t elem, const void* ptr, int64_t rows,
-                    int64_t cols, uint32_t box_cols, uint32_t box_rows) {
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, dtype, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(CCE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-  return CCE_OK;
-}
-
-#define CCE_TRY(expr)                                \
-  do {                                               \
-    cudaError_t e_ = (expr);                         \
-    if (e_ != cudaSuccess) return cuda_fail(e_, #expr); \
-  } while (0)
-
-#define CCE_CHECK(expr)            \
-  do {                             \
-    cce_status s_ = (expr);        \
-    if (s_ != CCE_OK) return s_;   \
-  } while (0)
-
 
 // The backward: plan the tiles and work lists, then one persistent launch (cce_bwd.cu) forms the
-// gradient tiles chunk by chunk and runs the dC and dE MMAs from them.
+// gradient tiles chunk by chunk and runs the dC and dE MMAs from them. With `lp`, of the
+// log-probabilities: the rows' coefficients and the tokens come from logprob_prep_kernel, which also
+// copies E with the rows that ask for nothing zeroed, so that what stands in them (padding, NaN)
+// reaches no product. The plan then sees rows that are scored but have no target of their own (id V of
+// V + 1), and keeps the units that hold a given token.
 cce_status backward_split(const cce_problem* p, const void* E, const void* C, const void* bias, const int64_t* targets,
                           const float* lse, const float* tile_max, const int64_t* count, const float* grad_out,
                           float filter_eps, void* dE, void* dC, void* dbias, int32_t out_fp32,
-                          int64_t* filtered_tiles, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+                          int64_t* filtered_tiles, void* workspace, size_t workspace_bytes, cudaStream_t s,
+                          const cce::LogprobGrads* lp = nullptr) {
   const SplitWs w = carve_split(p, out_fp32, workspace);
-  if (workspace_bytes < w.bytes)
-    return fail(CCE_ERR_WORKSPACE, "backward workspace is %zu bytes, needs %zu", workspace_bytes, w.bytes);
+  const LogprobWs lw = lp != nullptr ? carve_logprob(p, lp->K, w.bytes, workspace) : LogprobWs{};
+  const size_t need = lp != nullptr ? lw.bytes : w.bytes;
+  if (workspace_bytes < need)
+    return fail(CCE_ERR_WORKSPACE, "backward workspace is %zu bytes, needs %zu", workspace_bytes, need);
   int num_sms = 0;
   CCE_CHECK(check_device(&num_sms));
   CCE_CHECK(get_encoder());
@@ -328,8 +353,31 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
     return cudaMemsetAsync(filtered_tiles, 0, sizeof(int64_t), s) == cudaSuccess ? CCE_OK
                                                                                   : fail(CCE_ERR_CUDA, "memset");
   }
+  if (lp != nullptr) {
+    cce::LogprobPrep P = lw.prep;
+    P.N = static_cast<int>(N);
+    P.D = static_cast<int>(D);
+    P.V = static_cast<int>(V);
+    P.K = lp->K;
+    P.tokens = lp->tokens;
+    P.ignore_index = lp->ignore_index;
+    P.inv_t = 1.f / lp->temperature;
+    P.lse_in = lp->lse;
+    P.entropy = lp->entropy;
+    P.g_logprobs = lp->g_logprobs;
+    P.g_entropy = lp->g_entropy;
+    P.E = static_cast<const __nv_bfloat16*>(E);
+    P.masked_id = p->ignore_index;
+    CCE_TRY(cce::launch_logprob_prep(P, s));
+    targets = lw.prep.targets;
+    lse = lw.prep.lse;
+    grad_out = lw.prep.one;
+    E = lw.prep.E_out;
+  }
   {
     cce::PlanArgs PA{};
+    PA.tok = lp != nullptr ? lw.prep.tok : nullptr;
+    PA.K = lp != nullptr ? lp->K : 0;
     PA.sync = w.sync;
     PA.sync_ints = static_cast<int64_t>(w.sync_bytes / sizeof(int));
     PA.P = w.plan;
@@ -449,6 +497,14 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   A.ctr_g_b = 0;
   A.ctr_g_t = w.plan.nchunks * w.plan.nb;
   A.ctr_b_done = A.ctr_g_t + w.plan.nt;
+  if (lp != nullptr) {
+    A.lp_coef = lw.prep.coef;
+    A.lp_coef_log = lw.prep.coef_log;
+    A.lp_tok = lw.prep.tok;
+    A.lp_tok_g = lw.prep.tok_g;
+    A.lp_k = lp->K;
+    A.lp_inv_t = 1.f / lp->temperature;
+  }
   A.err = &w.hdr->err;
   A.timeout_ns = cce::wait_timeout_ns();
   // Failure-detection test hook: CCE_TEST_INJECT_STALL=2 makes the backward's dE items of the first
@@ -506,6 +562,19 @@ uint64_t wait_timeout_ns() {
   return static_cast<uint64_t>(ms * 1e6);
 }
 void set_last_error(const char* msg) { g_last_error = msg; }
+
+size_t logprobs_backward_bytes(const cce_problem* p, int K, int32_t out_fp32) {
+  if (!problem_ok(p, true)) return 0;
+  return carve_logprob(p, K, carve_split(p, out_fp32, nullptr).bytes, nullptr).bytes;
+}
+
+cce_status logprobs_backward(const cce_problem* p, const LogprobGrads& g, const void* E, const void* C, const void* bias,
+                             const float* tile_max, float filter_eps, void* dE, void* dC, void* dbias, int32_t out_fp32,
+                             int64_t* filtered_tiles, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+  if (!problem_ok(p, true)) return CCE_ERR_INVALID_ARG;
+  return backward_split(p, E, C, bias, g.tokens, g.lse, tile_max, filtered_tiles, nullptr, filter_eps, dE, dC, dbias,
+                        out_fp32, filtered_tiles, workspace, workspace_bytes, s, &g);
+}
 }  // namespace cce
 
 extern "C" {

@@ -229,6 +229,11 @@ __device__ __forceinline__ void decode_item(int w, int g, int g_begin, int nchun
   }
 }
 
+// LP: the quads form the gradient of log-probabilities and entropy (see LogprobPrep) instead of the loss's:
+// G = p (coef + coef_log ln p) + sum_k tok_g[k] [v = t_k], p = exp(S / T - LSE), in fp32, rounded to bf16
+// once: the tokens' terms are added before the rounding, so that g (1 - p) of a confident token keeps its
+// leading bits.
+template <bool LP>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tmE128, const __grid_constant__ CUtensorMap tmC128,
                const __grid_constant__ CUtensorMap tmE64, const __grid_constant__ CUtensorMap tmC64,
@@ -515,8 +520,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (it.kind == kQuad) {
         const int b = it.key;
         const int r = b * BM + row;
-        const float lse_r = (r < A.N) ? A.lse[r] : 0.f;
+        const float lse_r = (r < A.N) ? A.lse[r] : (LP ? INFINITY : 0.f);
         const float lse_l2 = lse_r * kLog2e;
+        const float lp_coef = (LP && r < A.N) ? A.lp_coef[r] : 0.f;
+        const float lp_log2 = (LP && r < A.N) ? A.lp_coef_log[r] * 0.6931471805599453f : 0.f;
+        const float lp_scale = LP ? A.lp_inv_t * kLog2e : 0.f;
+        const int lp_tok0 = (LP && r < A.N) ? A.lp_tok[r] : -1;
         const float sc = (r < A.N) ? A.scale[r] : 0.f;
         const float sc_p = sc * fmaf(2.f * A.z_loss, lse_r, 1.f);  // softmax part: (1 + 2 zl LSE) p
         const float sc_y = sc * A.onehot_coef;                     // onehot part: (1 - ls) y
@@ -553,12 +562,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const int col0 = vb + c * 32;
               tmem_ld32(tmem_base + lane_off + static_cast<uint32_t>(a * 2 * BN + j * kSubTile + c * 32), v);
               if (A.bias != nullptr) add_bias32(v, A.bias, col0, A.V);
+              if constexpr (LP) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = sc_p * exp2f(fmaf(v[e], kLog2e, -lse_l2));
+                for (int e = 0; e < 32; ++e) {
+                  const float l2 = fmaf(v[e], lp_scale, -lse_l2);  // log2 p; p = 0 far below -200
+                  v[e] = exp2f(l2) * fmaf(lp_log2, fmaxf(l2, -200.f), lp_coef);
+                }
+                for (int k = 0; k < A.lp_k; ++k) {
+                  const int id = k == 0 ? lp_tok0 : (r < A.N ? A.lp_tok[static_cast<int64_t>(k) * A.N + r] : -1);
+                  const int at = id - col0;
+                  const bool hit = id >= 0 && at >= 0 && at < 32;
+                  if (__any_sync(0xffffffffu, hit)) {
+                    const float gk = hit ? A.lp_tok_g[static_cast<int64_t>(k) * A.N + r] : 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                if (c * 32 + e == tcol) v[e] -= sc_y;
-                if (col0 + e >= A.V) v[e] = 0.f;
+                    for (int e = 0; e < 32; ++e) v[e] += e == at ? gk : 0.f;
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (col0 + e >= A.V) v[e] = 0.f;
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = sc_p * exp2f(fmaf(v[e], kLog2e, -lse_l2));
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  if (c * 32 + e == tcol) v[e] -= sc_y;
+                  if (col0 + e >= A.V) v[e] = 0.f;
+                }
               }
 #pragma unroll
               for (int h = 0; h < 4; ++h) {
@@ -793,19 +823,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_bwd(const BwdLaunch& L, bool after_kernel, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+namespace {
+
+template <bool LP>
+cudaError_t launch_one(const BwdLaunch& L, bool after_kernel, cudaStream_t s) {
+  auto kernel = bwd_kernel<LP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if (after_kernel) {
-    e = launch_after_previous(bwd_kernel, dim3(L.num_sms), dim3(NUM_THREADS), SMEM_BYTES, s, L.tmE128, L.tmC128,
-                              L.tmE64, L.tmC64, L.tmdC, L.tmdE, L.args);
+    e = launch_after_previous(kernel, dim3(L.num_sms), dim3(NUM_THREADS), SMEM_BYTES, s, L.tmE128, L.tmC128, L.tmE64,
+                              L.tmC64, L.tmdC, L.tmdE, L.args);
     if (e != cudaSuccess) return e;
   } else {
-    bwd_kernel<<<L.num_sms, NUM_THREADS, SMEM_BYTES, s>>>(L.tmE128, L.tmC128, L.tmE64, L.tmC64, L.tmdC, L.tmdE,
-                                                           L.args);
+    kernel<<<L.num_sms, NUM_THREADS, SMEM_BYTES, s>>>(L.tmE128, L.tmC128, L.tmE64, L.tmC64, L.tmdC, L.tmdE, L.args);
   }
   note_launches(1);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_bwd(const BwdLaunch& L, bool after_kernel, cudaStream_t s) {
+  return L.args.lp_coef != nullptr ? launch_one<true>(L, after_kernel, s) : launch_one<false>(L, after_kernel, s);
 }
 
 }  // namespace cce

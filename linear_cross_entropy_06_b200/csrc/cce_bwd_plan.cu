@@ -6,6 +6,7 @@
 // README, "How it works" item 2: skip tiles whose softmax is below 2^-12), judged from the forward's
 // saved per-64-column maxima. A tile (128 x 128) with a kept half is listed; only its kept halves are
 // recomputed and multiplied into dE, and its skipped half reads as zeros in the dC MMAs.
+// For log-probabilities of given tokens a half that holds one of them is kept too (PlanArgs.tok).
 // The onehot term of p - y (Loss functions explainer, "How it works" item 2) is never skipped. A row
 // whose target lies in a skipped half (of a listed tile, or of a tile with no kept half, "onehot
 // only") gets its onehot term one row at a time, listed by vocabulary tile in oh_off / oh_rows (dC
@@ -165,11 +166,13 @@ __device__ __forceinline__ float warp_column_max32(float (&v)[32], int lane) {
 __device__ void tile_flags_unit(const PlanArgs& A, int group, int b, int t0) {
   __shared__ float wmax[kFlagGroups][4][2 * kFlagTiles];
   __shared__ int any_target[kFlagGroups][kFlagTiles];
+  __shared__ unsigned forced[kFlagGroups];  // halves that hold a given token (log-probabilities)
   const int tid = threadIdx.x & (kBwdBM - 1), lane = tid & 31;
   const int nt = A.P.nt;
   const int64_t r = static_cast<int64_t>(b) * kBwdBM + tid;
   const bool row_in = r < A.N;
   if (tid < kFlagTiles) any_target[group][tid] = 0;
+  if (tid == 0) forced[group] = 0;
   const int64_t j0 = 2 * static_cast<int64_t>(t0);  // the run's first half (saved sub-tile)
   float mt[2 * kFlagTiles];
 #pragma unroll
@@ -182,6 +185,12 @@ __device__ void tile_flags_unit(const PlanArgs& A, int group, int b, int t0) {
   const bool local = valid && valid_target(tr - A.vs, A.V, A.ignore_index - A.vs);  // its target is in this shard
   tr -= A.vs;
   if (local && tr / kBwdBN >= t0 && tr / kBwdBN < t0 + kFlagTiles) any_target[group][tr / kBwdBN - t0] = 1;
+  if (A.tok != nullptr && A.filter_on && row_in) {
+    for (int k = 0; k < A.K; ++k) {
+      const int64_t h = A.tok[static_cast<int64_t>(k) * A.N + r] / kSubTile - j0;
+      if (A.tok[static_cast<int64_t>(k) * A.N + r] >= 0 && h >= 0 && h < 2 * kFlagTiles) atomicOr(&forced[group], 1u << h);
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 2 * kFlagTiles; ++k) mt[k] = valid ? mt[k] - l : -INFINITY;
   wmax[group][tid >> 5][lane] = warp_column_max32(mt, lane);  // lane k: the warp's max of half j0 + k
@@ -192,7 +201,7 @@ __device__ void tile_flags_unit(const PlanArgs& A, int group, int b, int t0) {
     for (int h = 0; h < 2; ++h) {
       const int k = 2 * tid + h;
       const float m = fmaxf(fmaxf(wmax[group][0][k], wmax[group][1][k]), fmaxf(wmax[group][2][k], wmax[group][3][k]));
-      if (j0 + k < A.T && (!A.filter_on || m >= A.ln_eps)) halves |= 1 << h;
+      if (j0 + k < A.T && (!A.filter_on || m >= A.ln_eps || ((forced[group] >> k) & 1u))) halves |= 1 << h;
     }
     A.P.flags[static_cast<int64_t>(b) * nt + t0 + tid] = static_cast<uint8_t>(
         halves != 0 ? (kFlagListed | (halves << 2)) : (any_target[group][tid] ? kFlagOnehotOnly : 0));

@@ -1,0 +1,115 @@
+// Internal interface of the head operators (log-probabilities of given tokens with entropy, top
+// alternatives, the 8-bit product): the kernels of cce_head.cu and their host side in cce_head_api.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <stdint.h>
+
+namespace cce {
+
+constexpr int kHeadBM = 128;       // rows of a logit tile
+constexpr int kHeadBN = 256;       // vocabulary columns of a logit tile
+constexpr int kHeadGroup = 32;     // row blocks that walk the vocabulary together (their E stays in L2)
+constexpr int kHeadMaxTokens = 32; // given tokens a row
+constexpr int kHeadMaxTop = 24;    // alternatives a row
+constexpr int kHeadShortList = 12; // candidates kept for up to 8 alternatives, and for more: at least 4 to spare,
+constexpr int kHeadLongList = 28;  // see head_finish_kernel
+
+// How the logit tiles are split over the blocks of the grid. Row blocks are taken in `ngroups` groups of
+// nearly equal size. A group's work is the list of its units (`unit` vocabulary columns of one row
+// block), row block by row block; block c of the P = min(grid, units) that take part gets the units
+// [c U / P, (c + 1) U / P). What a block gets of one row block is a segment: it keeps the softmax
+// statistics (and the best alternatives) of the segment on chip and writes them once.
+struct HeadSplit {
+  int nb;       // row blocks
+  int nu;       // units of a row block
+  int unit;     // columns of a unit: a multiple of 32
+  int ngroups;
+  int grid;
+
+  __host__ __device__ int group_begin(int g) const {
+    return static_cast<int>(static_cast<long long>(nb) * g / ngroups);
+  }
+  __host__ __device__ int units(int rows) const { return rows * nu; }
+  __host__ __device__ int parts(int total) const { return total < grid ? total : grid; }
+  __host__ __device__ static int part_begin(int c, int total, int P) {
+    return static_cast<int>(static_cast<long long>(total) * c / P);
+  }
+  // The block that gets unit x: the largest c with part_begin(c) <= x.
+  __host__ __device__ static int owner(int x, int total, int P) {
+    return static_cast<int>(((static_cast<long long>(x) + 1) * P - 1) / total);
+  }
+  // At most this many segments a row block.
+  __host__ __device__ int max_segments() const {
+    const int rows = nb / ngroups < 1 ? 1 : nb / ngroups;  // the smallest group
+    return (grid + rows - 1) / rows + 1;
+  }
+};
+
+struct HeadArgs {
+  HeadSplit split;
+  int N, D, V;
+  int num_kb;    // K-blocks of 128 bytes
+  int kb_chunk;  // K-blocks summed in one tensor-memory accumulator
+  int box_c;     // rows of C a TMA box
+  int e_rows;    // rows of E a TMA box
+  const __nv_bfloat16* bias;  // [V] or null
+  const float* e_scale;       // [N], [V]: scales of 8-bit operands
+  const float* c_scale;
+  const int64_t* tokens;      // [N, K]
+  int64_t ignore_index;
+  int K;
+  float* zt;        // [K, N]: logits of the given tokens
+  float* tile_max;  // [ceil(V / 64), N]: largest y of each 64 columns, or null
+  float inv_t;      // 1 / temperature
+  float* part_m;    // [2 segments, N]: largest logit, sum of exp, sum of (y - largest y) log2 e exp
+  float* part_s;
+  float* part_w;
+  unsigned long long* lists;  // [2 segments, N, L]: best keys, highest first
+  void* out;        // [N, V] logits (8-bit product)
+  int out_fp32;
+  int* err;
+  uint64_t timeout_ns;
+  int inject_stall;
+};
+
+struct HeadFinish {
+  HeadSplit split;
+  int N, D, V;
+  const __nv_bfloat16* E;  // for the order of close alternatives: bf16 operands, or the 8-bit ones
+  const __nv_bfloat16* C;
+  const int8_t* E8;
+  const int8_t* C8;
+  const float* e_scale;
+  const float* c_scale;
+  const __nv_bfloat16* bias;
+  const int64_t* tokens;
+  int64_t ignore_index;
+  int K;
+  const float* zt;
+  float inv_t;
+  const float* part_m;
+  const float* part_s;
+  const float* part_w;
+  const unsigned long long* lists;
+  int L;  // entries of a list (0: no alternatives)
+  int top_k;
+  float* logprobs;   // [N, K]
+  float* entropy;    // [N]
+  float* lse;        // [N]
+  float* top_logprobs;  // [N, top_k]
+  int64_t* top_ids;
+  int* err;
+};
+
+cudaError_t launch_head(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool int8, int list_len,
+                        bool after_kernel, cudaStream_t s);
+cudaError_t launch_head_finish(const HeadFinish& F, bool after_kernel, cudaStream_t s);
+// Rows of 8-bit integers: scale = max |x| / 127, q = x / scale to the nearest integer.
+cudaError_t launch_quantize_rows(const __nv_bfloat16* x, int64_t rows, int64_t D, int8_t* q, float* scale,
+                                 cudaStream_t s);
+
+}  // namespace cce

@@ -1,0 +1,344 @@
+// C ABI of the head operators (declared in include/cce.h): log-probabilities of given tokens with
+// entropy and top alternatives, their backward, and the product with a classifier of 8-bit integers.
+// Argument checks, workspace carving, tensor maps and the launches. Host code only.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
+
+#include "cce.h"
+#include "cce_head.h"
+#include "cce_host.h"
+#include "cce_internal.h"
+
+namespace {
+
+using cce::aligned16;
+using cce::align_up;
+using cce::ceil_div;
+using cce::fail;
+
+// Largest width of 8-bit operands: 127 * 127 * D stays below 2^31.
+constexpr int64_t kInt8MaxD = 131072;
+// K-blocks (of 64 values) summed in one accumulator: see the head of cce_head.cu. 512 values.
+constexpr int kChunkBlocks = 8;
+
+bool sizes_ok(int64_t N, int64_t D, int64_t V, bool int8, bool set_error) {
+  auto bad = [&](const char* msg) {
+    if (set_error) fail(CCE_ERR_INVALID_ARG, "%s", msg);
+    return false;
+  };
+  if (N < 0) return bad("N must be >= 0");
+  if (V < 1) return bad("V must be >= 1");
+  if (int8 && (D < 16 || D % 16 != 0)) return bad("D must be a positive multiple of 16 for 8-bit operands");
+  if (int8 && D > kInt8MaxD) return bad("D too large for 8-bit operands");
+  if (D < 8 || D % 8 != 0) return bad("D must be a positive multiple of 8");
+  if (N >= (int64_t(1) << 31) - 256 || V >= (int64_t(1) << 31) - 256 || D >= (int64_t(1) << 24))
+    return bad("N, V or D too large");
+  return true;
+}
+
+bool logprobs_ok(const cce_logprob_problem* p, bool set_error) {
+  auto bad = [&](const char* msg) {
+    if (set_error) fail(CCE_ERR_INVALID_ARG, "%s", msg);
+    return false;
+  };
+  if (p == nullptr) return bad("problem is NULL");
+  if (!sizes_ok(p->N, p->D, p->V, p->int8 != 0, set_error)) return false;
+  if (p->int8 != 0 && p->int8 != 1) return bad("int8 must be 0 or 1");
+  if (p->num_tokens < 0 || p->num_tokens > cce::kHeadMaxTokens) return bad("num_tokens must be in [0, 32]");
+  if (p->top_k < 0 || p->top_k > cce::kHeadMaxTop) return bad("top_k must be in [0, 24]");
+  if (p->top_k > p->V) return bad("top_k must not exceed V");
+  if (p->num_tokens == 0 && p->top_k == 0) return bad("num_tokens and top_k are both 0: nothing to compute");
+  if (!(p->temperature > 0.f && p->temperature < INFINITY)) return bad("temperature must be finite and > 0");
+  if (!(1.f / p->temperature < INFINITY)) return bad("temperature too small");
+  if (p->reserved != 0) return bad("reserved must be 0");
+  return true;
+}
+
+// The split of the logit tiles over `sms` blocks. With at least kWideTiles tiles a block, units of a whole tile:
+// one load a stage brings 256 rows of C, and a block's share is uneven by at most one tile in that many. With fewer,
+// units of 32 columns (64 where maxima of 64 columns are kept), loaded 32 rows at a time, so that the blocks' shares
+// of C stay even: one row block on 148 SMs gets 27.1 units of 32 columns (at most 28) instead of 3.4 tiles (at
+// most 4).
+constexpr int64_t kWideTiles = 12;
+
+cce::HeadSplit make_split(int64_t N, int64_t V, bool maxima, int sms) {
+  cce::HeadSplit S{};
+  S.nb = static_cast<int>(ceil_div(N, cce::kHeadBM));
+  S.ngroups = static_cast<int>(ceil_div(S.nb, cce::kHeadGroup));
+  S.grid = sms;
+  const int64_t rows = std::max<int64_t>(S.nb / std::max(S.ngroups, 1), 1);
+  const bool wide = rows * ceil_div(V, cce::kHeadBN) >= kWideTiles * sms;
+  S.unit = wide ? cce::kHeadBN : (maxima ? 64 : 32);
+  S.nu = static_cast<int>(ceil_div(V, S.unit));
+  return S;
+}
+
+int list_len(int top_k) {
+  return top_k == 0 ? 0 : top_k <= cce::kHeadShortList - 4 ? cce::kHeadShortList : cce::kHeadLongList;
+}
+
+constexpr int kMaxSms = 148;  // the workspace is sized for a B200; a part with fewer SMs needs no more
+
+struct HeadWs {
+  cce::WsHeader* hdr;
+  float* zt;       // [K, N]
+  float* part_m;   // [2 segments, N] each
+  float* part_s;
+  float* part_w;
+  unsigned long long* lists;  // [2 segments, N, L]
+  int8_t* e8;      // [N, D]
+  float* e_scale;  // [N]
+  size_t bytes;
+};
+
+HeadWs carve(int64_t N, int64_t D, int64_t V, int K, int top_k, bool int8, bool stats, void* base) {
+  HeadWs w{};
+  char* b = static_cast<char*>(base);
+  size_t off = cce::kHeaderBytes;
+  auto take = [&](size_t bytes) {
+    char* ptr = b + off;
+    off = align_up(off + bytes);
+    return ptr;
+  };
+  const size_t n = static_cast<size_t>(N);
+  w.hdr = reinterpret_cast<cce::WsHeader*>(b);
+  if (stats && N > 0) {
+    const cce::HeadSplit S = make_split(N, V, false, kMaxSms);
+    const size_t parts = 2 * static_cast<size_t>(S.max_segments()) * n;
+    w.zt = reinterpret_cast<float*>(take(sizeof(float) * n * static_cast<size_t>(K)));
+    w.part_m = reinterpret_cast<float*>(take(sizeof(float) * parts));
+    w.part_s = reinterpret_cast<float*>(take(sizeof(float) * parts));
+    w.part_w = reinterpret_cast<float*>(take(sizeof(float) * parts));
+    w.lists = reinterpret_cast<unsigned long long*>(take(8 * parts * static_cast<size_t>(list_len(top_k))));
+  }
+  if (int8) {
+    w.e8 = reinterpret_cast<int8_t*>(take(n * static_cast<size_t>(D)));
+    w.e_scale = reinterpret_cast<float*>(take(sizeof(float) * n));
+  }
+  w.bytes = off;
+  return w;
+}
+
+// The arguments and tensor maps that every head launch shares.
+cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, const void* C, const void* bias,
+                     const float* c_scale, bool maxima, const HeadWs& w, int sms, cce::HeadArgs* A, CUtensorMap* tmE,
+                     CUtensorMap* tmC) {
+  A->split = make_split(N, V, maxima, std::min(sms, kMaxSms));
+  A->N = static_cast<int>(N);
+  A->D = static_cast<int>(D);
+  A->V = static_cast<int>(V);
+  const int per_block = int8 ? 128 : 64;  // values of a 128-byte K-block
+  A->num_kb = static_cast<int>(ceil_div(D, per_block));
+  A->kb_chunk = int8 ? A->num_kb : kChunkBlocks;
+  A->box_c = A->split.unit == cce::kHeadBN ? cce::kHeadBN : 32;
+  A->e_rows = static_cast<int>(std::min<int64_t>(cce::kHeadBM, (N + 7) / 8 * 8));
+  A->bias = static_cast<const __nv_bfloat16*>(bias);
+  A->e_scale = w.e_scale;
+  A->c_scale = c_scale;
+  A->err = &w.hdr->err;
+  A->timeout_ns = cce::wait_timeout_ns();
+  // Failure-detection test hook: CCE_TEST_INJECT_STALL=4 makes the first bounded wait of the head kernel run out
+  // (reported as CCE_ERR_DEVICE_TIMEOUT by cce_check_device_error).
+  const char* stall = std::getenv("CCE_TEST_INJECT_STALL");
+  A->inject_stall = (stall != nullptr && stall[0] == '4') ? 1 : 0;
+  const auto type = int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const size_t size = int8 ? 1 : 2;
+  const void* e = int8 ? static_cast<const void*>(w.e8) : E;
+  CCE_CHECK(cce::make_map(tmE, type, size, e, N, D, per_block, static_cast<uint32_t>(A->e_rows)));
+  CCE_CHECK(cce::make_map(tmC, type, size, C, V, D, per_block, static_cast<uint32_t>(A->box_c)));
+  return CCE_OK;
+}
+
+cce_problem backward_problem(const cce_logprob_problem* p) {
+  cce_problem q{};
+  q.N = p->N;
+  q.D = p->D;
+  q.V = p->V;
+  q.ignore_index = -100;
+  q.reduction = CCE_REDUCTION_SUM;
+  q.vocab_start = 0;
+  q.vocab_total = p->V + 1;  // id V: a row that is scored but has no target of its own
+  return q;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t cce_logprobs_workspace_size(const cce_logprob_problem* p) {
+  if (!logprobs_ok(p, false)) return 0;
+  return carve(p->N, p->D, p->V, p->num_tokens, p->top_k, p->int8 != 0, true, nullptr).bytes;
+}
+
+cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void* C, const float* c_scale,
+                        const void* bias, const int64_t* tokens, float* logprobs, float* entropy, float* lse,
+                        float* tile_max, float* top_logprobs, int64_t* top_ids, void* workspace, size_t workspace_bytes,
+                        cce_stream_t stream) {
+  cce::clear_last_error();
+  if (!logprobs_ok(p, true)) return CCE_ERR_INVALID_ARG;
+  const bool int8 = p->int8 != 0;
+  const bool has_rows = p->N > 0;
+  if (C == nullptr || workspace == nullptr || (int8 && c_scale == nullptr) ||
+      (has_rows && (E == nullptr ||
+                    (p->num_tokens > 0 &&
+                     (tokens == nullptr || logprobs == nullptr || entropy == nullptr || lse == nullptr)) ||
+                    (p->top_k > 0 && (top_logprobs == nullptr || top_ids == nullptr)))))
+    return fail(CCE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(E) || !aligned16(C) || !aligned16(c_scale) || !aligned16(bias) || !aligned16(workspace))
+    return fail(CCE_ERR_INVALID_ARG, "E, C, c_scale, bias and workspace must be 16-byte aligned");
+  const HeadWs w = carve(p->N, p->D, p->V, p->num_tokens, p->top_k, int8, true, workspace);
+  if (workspace_bytes < w.bytes)
+    return fail(CCE_ERR_WORKSPACE, "workspace is %zu bytes, needs %zu", workspace_bytes, w.bytes);
+  int sms = 0;
+  CCE_CHECK(cce::check_device(&sms));
+  CCE_CHECK(cce::get_encoder());
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(cce::WsHeader), s));
+  if (!has_rows) return CCE_OK;
+
+  if (int8)
+    CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), p->N, p->D, w.e8, w.e_scale, s));
+  cce::HeadArgs A{};
+  CUtensorMap tmE, tmC;
+  CCE_CHECK(head_args(p->N, p->D, p->V, int8, E, C, bias, c_scale, tile_max != nullptr, w, sms, &A, &tmE, &tmC));
+  A.tokens = tokens;
+  A.ignore_index = p->ignore_index;
+  A.K = p->num_tokens;
+  A.zt = w.zt;
+  A.tile_max = tile_max;
+  A.inv_t = 1.f / p->temperature;
+  A.part_m = w.part_m;
+  A.part_s = w.part_s;
+  A.part_w = w.part_w;
+  A.lists = w.lists;
+  CCE_TRY(cce::launch_head(tmE, tmC, A, int8, list_len(p->top_k), int8, s));
+
+  cce::HeadFinish F{};
+  F.split = A.split;
+  F.N = A.N;
+  F.D = A.D;
+  F.V = A.V;
+  F.E = static_cast<const __nv_bfloat16*>(E);
+  F.C = int8 ? nullptr : static_cast<const __nv_bfloat16*>(C);
+  F.E8 = w.e8;
+  F.C8 = int8 ? static_cast<const int8_t*>(C) : nullptr;
+  F.e_scale = w.e_scale;
+  F.c_scale = c_scale;
+  F.bias = A.bias;
+  F.tokens = tokens;
+  F.ignore_index = p->ignore_index;
+  F.K = A.K;
+  F.zt = w.zt;
+  F.inv_t = A.inv_t;
+  F.part_m = w.part_m;
+  F.part_s = w.part_s;
+  F.part_w = w.part_w;
+  F.lists = w.lists;
+  F.L = list_len(p->top_k);
+  F.top_k = p->top_k;
+  F.logprobs = logprobs;
+  F.entropy = entropy;
+  F.lse = lse;
+  F.top_logprobs = top_logprobs;
+  F.top_ids = top_ids;
+  F.err = A.err;
+  CCE_TRY(cce::launch_head_finish(F, true, s));
+  return CCE_OK;
+}
+
+size_t cce_logprobs_backward_workspace_size(const cce_logprob_problem* p, int32_t out_fp32) {
+  if (!logprobs_ok(p, false) || p->int8 != 0 || p->num_tokens == 0 || out_fp32 < CCE_OUT_BF16 ||
+      out_fp32 > CCE_OUT_DE_FP32)
+    return 0;
+  const cce_problem q = backward_problem(p);
+  return cce::logprobs_backward_bytes(&q, p->num_tokens, out_fp32);
+}
+
+cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, const void* C, const void* bias,
+                                 const int64_t* tokens, const float* lse, const float* entropy, const float* tile_max,
+                                 const float* grad_logprobs, const float* grad_entropy, float filter_eps, void* dE,
+                                 void* dC, void* dbias, int32_t out_fp32, int64_t* filtered_tiles, void* workspace,
+                                 size_t workspace_bytes, cce_stream_t stream) {
+  cce::clear_last_error();
+  if (!logprobs_ok(p, true)) return CCE_ERR_INVALID_ARG;
+  if (p->int8 != 0) return fail(CCE_ERR_INVALID_ARG, "a classifier of 8-bit integers has no gradient");
+  if (p->num_tokens == 0) return fail(CCE_ERR_INVALID_ARG, "without given tokens there is nothing to differentiate");
+  const bool has_rows = p->N > 0;
+  if (C == nullptr || dC == nullptr || filtered_tiles == nullptr || workspace == nullptr ||
+      (has_rows && (E == nullptr || tokens == nullptr || lse == nullptr || entropy == nullptr || dE == nullptr ||
+                    (filter_eps > 0.f && tile_max == nullptr))))
+    return fail(CCE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(E) || !aligned16(C) || !aligned16(bias) || !aligned16(dE) || !aligned16(dC) || !aligned16(dbias) ||
+      !aligned16(workspace))
+    return fail(CCE_ERR_INVALID_ARG, "E, C, bias, dE, dC, dbias and workspace must be 16-byte aligned");
+  if (std::isnan(filter_eps)) return fail(CCE_ERR_INVALID_ARG, "filter_eps is NaN");
+  if (out_fp32 < CCE_OUT_BF16 || out_fp32 > CCE_OUT_DE_FP32)
+    return fail(CCE_ERR_INVALID_ARG, "out_fp32 must be CCE_OUT_BF16, CCE_OUT_FP32 or CCE_OUT_DE_FP32");
+  const cce_problem q = backward_problem(p);
+  cce::LogprobGrads g{};
+  g.tokens = tokens;
+  g.ignore_index = p->ignore_index;
+  g.K = p->num_tokens;
+  g.temperature = p->temperature;
+  g.lse = lse;
+  g.entropy = entropy;
+  g.g_logprobs = grad_logprobs;
+  g.g_entropy = grad_entropy;
+  return cce::logprobs_backward(&q, g, E, C, bias, tile_max, filter_eps, dE, dC, dbias, out_fp32, filtered_tiles,
+                                workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+cce_status cce_quantize_int8(const void* x, int64_t rows, int64_t D, int8_t* q, float* scale, cce_stream_t stream) {
+  cce::clear_last_error();
+  if (!sizes_ok(rows, D, 1, true, true)) return CCE_ERR_INVALID_ARG;
+  if (rows > 0 && (x == nullptr || q == nullptr || scale == nullptr))
+    return fail(CCE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(q)) return fail(CCE_ERR_INVALID_ARG, "x and q must be 16-byte aligned");
+  int sms = 0;
+  CCE_CHECK(cce::check_device(&sms));
+  CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(x), rows, D, q, scale,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+  return CCE_OK;
+}
+
+size_t cce_int8_linear_workspace_size(int64_t N, int64_t D, int64_t V) {
+  if (!sizes_ok(N, D, V, true, false)) return 0;
+  return carve(N, D, V, 0, 0, true, false, nullptr).bytes;
+}
+
+cce_status cce_int8_linear(int64_t N, int64_t D, int64_t V, const void* E, const int8_t* C, const float* c_scale,
+                           const void* bias, void* out, int32_t out_fp32, void* workspace, size_t workspace_bytes,
+                           cce_stream_t stream) {
+  cce::clear_last_error();
+  if (!sizes_ok(N, D, V, true, true)) return CCE_ERR_INVALID_ARG;
+  if (C == nullptr || c_scale == nullptr || workspace == nullptr || (N > 0 && (E == nullptr || out == nullptr)))
+    return fail(CCE_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned16(E) || !aligned16(C) || !aligned16(c_scale) || !aligned16(bias) || !aligned16(out) ||
+      !aligned16(workspace))
+    return fail(CCE_ERR_INVALID_ARG, "E, C, c_scale, bias, out and workspace must be 16-byte aligned");
+  if (out_fp32 != 0 && out_fp32 != 1) return fail(CCE_ERR_INVALID_ARG, "out_fp32 must be 0 or 1");
+  const HeadWs w = carve(N, D, V, 0, 0, true, false, workspace);
+  if (workspace_bytes < w.bytes)
+    return fail(CCE_ERR_WORKSPACE, "workspace is %zu bytes, needs %zu", workspace_bytes, w.bytes);
+  int sms = 0;
+  CCE_CHECK(cce::check_device(&sms));
+  CCE_CHECK(cce::get_encoder());
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(cce::WsHeader), s));
+  if (N == 0) return CCE_OK;
+  CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), N, D, w.e8, w.e_scale, s));
+  cce::HeadArgs A{};
+  CUtensorMap tmE, tmC;
+  CCE_CHECK(head_args(N, D, V, true, E, C, bias, c_scale, false, w, sms, &A, &tmE, &tmC));
+  A.inv_t = 1.f;
+  A.out = out;
+  A.out_fp32 = out_fp32;
+  CCE_TRY(cce::launch_head(tmE, tmC, A, true, 0, true, s));
+  return CCE_OK;
+}
+
+}  // extern "C"

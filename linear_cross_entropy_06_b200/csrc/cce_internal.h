@@ -193,6 +193,13 @@ struct BwdArgs {
   int* err;
   uint64_t timeout_ns;
   int inject_stall;  // test hook: the first dE item waits for a count no item produces
+  // Gradient of log-probabilities and entropy instead of the loss (lp_coef not null; see LogprobPrep)
+  const float* lp_coef;
+  const float* lp_coef_log;
+  const int* lp_tok;      // [lp_k, N]
+  const float* lp_tok_g;  // [lp_k, N]
+  int lp_k;
+  float lp_inv_t;         // 1 / temperature
 };
 
 struct BwdLaunch {
@@ -229,6 +236,8 @@ struct PlanArgs {
   int* bar;                // grid barrier counter, zero at launch
   int* err;
   uint64_t timeout_ns;
+  const int* tok;          // [K, N] given tokens (-1: none) whose units are always kept, or null
+  int K;
   int inject_stall;        // test hook: block 0 leaves before the first grid barrier, whose wait then runs out
 };
 // One cooperative launch: the row scales, the tile flags, both tile lists, the quad list, the
@@ -307,5 +316,33 @@ cudaError_t launch_shard_merge(const float* partials, int shards, const int64_t*
                                int64_t ignore_index, float label_smoothing, float z_loss, int reduction, float* loss,
                                float* lse, int64_t* count, cudaStream_t s);
 cudaError_t launch_fill_zero(void* dst, int64_t bytes, cudaStream_t s);
+
+// What the backward of the log-probabilities needs before its plan (cce_aux.cu, one launch). With
+// y = z / T, lp_k = y_{t_k} - lse, p = softmax(y) and the gradients g_k of lp_k and h of the entropy H:
+//   dz_v = (1 / T) (sum_k g_k [v = t_k] - p_v (sum_k g_k + h H + h ln p_v)).
+// Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and tok_g[k] = g_k / T for the tokens
+// tok[k] (-1: ignored). A row that asks for nothing, or has no finite logit, gets zeros and lse = +inf
+// (p = 0).
+struct LogprobPrep {
+  int N, D, V, K;
+  const int64_t* tokens;  // [N, K]
+  int64_t ignore_index;
+  float inv_t;
+  const float* lse_in;
+  const float* entropy;
+  const float* g_logprobs;  // [N, K] or null
+  const float* g_entropy;   // [N] or null
+  const __nv_bfloat16* E;
+  int64_t masked_id;        // targets[r] of a row that asks for nothing
+  float* coef;              // outputs
+  float* coef_log;
+  float* lse;
+  int* tok;
+  float* tok_g;
+  int64_t* targets;         // V for the other rows: scored, their target in no tile of C
+  float* one;               // [1] 1.0: the scale of every row's gradient
+  __nv_bfloat16* E_out;     // [N, D]
+};
+cudaError_t launch_logprob_prep(const LogprobPrep& P, cudaStream_t s);
 
 }  // namespace cce

@@ -55,9 +55,24 @@ class Problem(ctypes.Structure):
     ]
 
 
+class LogprobProblem(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int64),
+        ("D", ctypes.c_int64),
+        ("V", ctypes.c_int64),
+        ("ignore_index", ctypes.c_int64),
+        ("num_tokens", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("temperature", ctypes.c_float),
+        ("int8", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 # Every symbol include/cce.h declares, with its ctypes signature.
 _VP, _SZ, _I32, _I64, _F32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _PP = ctypes.POINTER(Problem)
+_LP = ctypes.POINTER(LogprobProblem)
 SIGNATURES = {
     "cce_tile_max_len": (_I64, [_PP]),
     "cce_backward_tile_shape": (None, [ctypes.POINTER(_I32), ctypes.POINTER(_I32)]),
@@ -76,6 +91,13 @@ SIGNATURES = {
     "cce_backward_skip_map": (_I32, [_PP, _VP, _SZ, _VP, _VP]),
     "cce_forward_partial": (_I32, [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "cce_forward_merge": (_I32, [_PP, _VP, _I32, _VP, _VP, _VP, _VP, _VP]),
+    "cce_logprobs_workspace_size": (_SZ, [_LP]),
+    "cce_logprobs": (_I32, [_LP] + [_VP] * 12 + [_SZ, _VP]),
+    "cce_logprobs_backward_workspace_size": (_SZ, [_LP, _I32]),
+    "cce_logprobs_backward": (_I32, [_LP] + [_VP] * 9 + [_F32, _VP, _VP, _VP, _I32, _VP, _VP, _SZ, _VP]),
+    "cce_quantize_int8": (_I32, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "cce_int8_linear_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "cce_int8_linear": (_I32, [_I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP]),
 }
 
 OUT_BF16, OUT_FP32, OUT_DE_FP32 = 0, 1, 2  # cce_backward's output dtype modes
