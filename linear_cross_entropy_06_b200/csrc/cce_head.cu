@@ -10,17 +10,20 @@
 // loses anything for large |z|: only differences to the maximum are exponentiated. A new maximum m' takes
 // S to S f and W to f (W + S d'), f = 2^d', d' = (m - m') log2(e) / temperature.
 //
-// Design (B200): one persistent block per SM, 12 warps.
+// Design (B200): one persistent block per SM, 20 warps.
 //   warp 0       producer: E and C K-blocks of 128 bytes (128B swizzle) by TMA into a 4-stage ring.
 //   warp 1       tensor memory owner; one lane issues tcgen05.mma, M = 128 rows, N = up to 256 columns.
-//   warps 4..11  epilogue, two warps for each 32 rows (one for each 128 columns of the tile): a thread owns
-//                128 logits of one row, in registers.
+//   warps 4..19  epilogue, four warps for each 32 rows (one for each 64 columns of the tile): a thread owns
+//                64 logits of one row, in registers. Four warps a scheduler hide the latency of tensor memory
+//                and of the exponentials; eight warps with 128 logits each were bound by it (2048 x 2048 x
+//                128256: 844 us).
 // Sums over K: the tensor cores add into their fp32 accumulator without rounding to nearest, so a long sum
 // drifts towards zero (D = 4096, logits of 11: -5e-5, sixteen times what fp32 sums lose). The accumulator is
 // therefore handed over every kb_chunk K-blocks (512 values of K) and the parts are added in registers, rounded
 // to nearest: two tensor-memory buffers alternate by parts, and the drift falls with the parts' number.
 // 8-bit products are exact in 32-bit integers, so they keep one part.
 #include <algorithm>
+#include <type_traits>
 
 #include "cce_device.cuh"
 #include "cce_head.h"
@@ -36,19 +39,20 @@ constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * KB_BYTES;
 constexpr int B_BYTES = BN * KB_BYTES;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int NUM_THREADS = 384;
-constexpr int EPI_THREADS = 256;
+constexpr int EPI_WARPS = 16;
+constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
+constexpr int COLS = BN / (EPI_WARPS / 4);  // columns of a thread
 constexpr int TMEM_COLS = 512;
 constexpr int NUM_BARRIERS = 2 * STAGES + 4 + 1;
-constexpr int SCRATCH_WARP = 4096;  // of each epilogue warp: its rows' tokens, or a piece of the logits on its way out
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 8 * SCRATCH_WARP + NUM_BARRIERS * 8 + 16;
+constexpr int SCRATCH_WARP = 2048;  // of each epilogue warp: a piece of the logits on its way out
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * SCRATCH_WARP + NUM_BARRIERS * 8 + 16;
 static_assert(SMEM_BYTES <= 232448, "fits the 227 KB opt-in shared memory of an SM");
-static_assert(kHeadMaxTokens * 32 * 4 <= SCRATCH_WARP, "the tokens of a warp's 32 rows fit its scratch");
+static_assert(COLS == kSubTile && COLS == 4 * kHeadPick, "a thread's columns are one saved maximum, and four picks");
 
-// Registers a thread: 384 threads are launched with 168 each; the first warpgroup hands 128 of its own to the two
-// that hold logits and lists in registers (56 x 128 + 224 x 256 = 168 x 384).
-constexpr int REGS_FEW = 40, REGS_MANY = 232;
-static_assert(REGS_FEW * 128 + REGS_MANY * 256 <= 168 * 384, "setmaxnreg draws on the launch's registers");
+// Registers a thread: 640 threads are launched with 96 each; the first warpgroup hands 32 of its own to the four that
+// hold logits in registers.
+constexpr int REGS_FEW = 64, REGS_MANY = 104;
+static_assert(REGS_FEW * 128 + REGS_MANY * 512 <= 96 * 640, "setmaxnreg draws on the launch's registers");
 
 template <int R>
 __device__ __forceinline__ void regs_inc() {
@@ -78,7 +82,7 @@ __device__ __forceinline__ uint32_t idesc_n(bool int8, int n) {
 }
 
 // 32 lanes x 16 consecutive columns of tensor memory.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -130,17 +134,18 @@ struct HeadTile {
   bool first, last;  // of the segment
 };
 
-// Calls f(tile) for every tile of block c, in the order that all roles share; f returns false to stop. Within a
+// Calls f(tile) for every tile of this block, in the order that all roles share; f returns false to stop. Within a
 // segment the walk starts at the tile whose position is 0 modulo the length of a block's share: the blocks on
 // different row blocks then pass the same columns of C at about the same time, and C is read from HBM about once
 // a group.
 template <typename F>
-__device__ __forceinline__ void for_tiles(const HeadSplit& S, int V, int c, F&& f) {
+__device__ __forceinline__ void for_tiles(const HeadSplit& S, int V, F&& f) {
   for (int g = 0; g < S.ngroups; ++g) {
-    int x, hi;
+    int x, hi, c;
     {
-      const int total = S.units(S.group_begin(g + 1) - S.group_begin(g)), P = S.parts(total);
-      if (c >= P) continue;
+      const int gb = S.group_begin(g + 1) - S.group_begin(g), total = S.units(gb), P = S.parts(total);
+      if (static_cast<int>(blockIdx.x) >= P) continue;
+      c = S.order[gb == S.nb / S.ngroups ? 0 : 1][blockIdx.x];
       x = HeadSplit::part_begin(c, total, P);
       hi = HeadSplit::part_begin(c + 1, total, P);
     }
@@ -173,46 +178,124 @@ __device__ __forceinline__ void for_tiles(const HeadSplit& S, int V, int c, F&& 
   }
 }
 
-// v[i] = c_scale[col0 + i] (columns from `limit` on: 0), 32 columns from a multiple of 32.
-__device__ __forceinline__ void load_scale32(float (&v)[32], const float* scale, int col0, int limit) {
-  if (col0 + 32 <= limit) {
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Adds sum 2^d and sum d 2^d, d = (a - m) sc, of a thread's columns. MASKED: some a may be -inf; its power is 0, and
+// with d held above -1e4 (where the power is 0 too) so is its product with d.
+template <bool MASKED>
+__device__ __forceinline__ void add_powers(const float (&a)[COLS], float m, float sc, float& s, float& w) {
+  const uint64_t mm = pack2(-m, -m), cc = pack2(sc, sc);
+  uint64_t s2 = 0, w2 = 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint4 u = ld_global_nc_v4(scale + col0 + 4 * q);
-      v[4 * q] = __uint_as_float(u.x);
-      v[4 * q + 1] = __uint_as_float(u.y);
-      v[4 * q + 2] = __uint_as_float(u.z);
-      v[4 * q + 3] = __uint_as_float(u.w);
+  for (int i = 0; i < COLS; i += 2) {
+    const uint64_t d2 = mul2(add2(pack2(a[i], a[i + 1]), mm), cc);
+    float d0, d1;
+    unpack2(d2, d0, d1);
+    if (MASKED) {
+      d0 = max_nan(d0, -1e4f);
+      d1 = max_nan(d1, -1e4f);
     }
-  } else {
+    const uint64_t e2 = pack2(ex2(d0), ex2(d1));
+    s2 = add2(s2, e2);
+    w2 = fma2(MASKED ? pack2(d0, d1) : d2, e2, w2);
+  }
+  float x, y;
+  unpack2(s2, x, y);
+  s += x + y;
+  unpack2(w2, x, y);
+  w += x + y;
+}
+
+// Writes a warp's 32 rows x COLS columns of logits. A thread's own 32 bytes of a row at a time where rows start on
+// 32-byte boundaries (whole sectors); else 32 columns at a time through the warp's scratch, so that the warp
+// writes runs of one row.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void write_logits(const HeadArgs& A, const float (&a)[COLS], int row0, int col0, int ncol,
+                                             int lane, uint8_t* scratch) {
+  const int per_sector = A.out_fp32 ? 8 : 16;
+  if (A.V % per_sector == 0 && (reinterpret_cast<uintptr_t>(A.out) & 31u) == 0 && ncol % per_sector == 0) {
+    if (row0 + lane >= A.N) return;
+    const int64_t o = static_cast<int64_t>(row0 + lane) * A.V + col0;
+    if (A.out_fp32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = col0 + i < limit ? scale[col0 + i] : 0.f;
+      for (int j = 0; j < COLS / 8; ++j) {
+        if (8 * j >= ncol) break;
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(a[8 * j + i]);
+        store32(static_cast<float*>(A.out) + o + 8 * j, u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < COLS / 16; ++j) {
+        if (16 * j >= ncol) break;
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(a[16 * j + 2 * i], a[16 * j + 2 * i + 1]);
+        store32(static_cast<__nv_bfloat16*>(A.out) + o + 16 * j, u);
+      }
+    }
+    return;
+  }
+  const int n_rows = min(32, A.N - row0);
+#pragma unroll
+  for (int j = 0; j < COLS / 16; ++j) {
+    if (16 * j >= ncol) break;
+    // 32 rows x 16 columns, column c of row k at word 16 k + (c + k / 2) % 16: no bank meets twice on the way in
+    float* st = reinterpret_cast<float*>(scratch);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st[lane * 16 + ((i + (lane >> 1)) & 15)] = a[16 * j + i];
+    __syncwarp();
+    const int c = lane & 15;
+    for (int k = lane >> 4; k < n_rows; k += 2) {  // two rows a step
+      const float v = st[k * 16 + ((c + (k >> 1)) & 15)];
+      const int64_t o = static_cast<int64_t>(row0 + k) * A.V + col0 + 16 * j + c;
+      if (16 * j + c < ncol) {
+        if (A.out_fp32) static_cast<float*>(A.out)[o] = v;
+        else static_cast<__nv_bfloat16*>(A.out)[o] = __float2bfloat16_rn(v);
+      }
+    }
   }
 }
 
-// a[i] of 32 registers, i in the lane's own register: five levels of selection.
-__device__ __forceinline__ float pick32(const float* a, int i) {
-  float t16[16], t8[8], t4[4], t2[2];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) t16[k] = (i & 16) ? a[k + 16] : a[k];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) t8[k] = (i & 8) ? t16[k + 8] : t16[k];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) t4[k] = (i & 4) ? t8[k + 4] : t8[k];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) t2[k] = (i & 2) ? t4[k + 2] : t4[k];
-  return (i & 1) ? t2[1] : t2[0];
-}
-
-// L: entries of a thread's list of best keys (0: none). OUT: the logits are written out instead of reduced.
-template <bool I8, int L, bool OUT>
+// OUT: the logits are written out instead of reduced.
+template <bool I8, bool OUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     head_kernel(const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmC,
                 const __grid_constant__ HeadArgs A) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* scratch = base + STAGES * STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + 8 * SCRATCH_WARP);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + EPI_WARPS * SCRATCH_WARP);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,7 +313,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), EPI_THREADS);
+      mbar_init(tempty_bar(a), EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -244,233 +327,140 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  wait_for_previous_grid();  // the 8-bit rows of E, when a kernel of this call made them
+  wait_for_previous_grid();  // the 8-bit rows of E or the transposed tokens, when a kernel of this call made them
   const WaitCtl wc{abort_flag, A.err, A.timeout_ns};
   const int num_kb = A.num_kb;
   constexpr int KE = I8 ? KB_BYTES : KB_BYTES / 2;  // values of K a block
 
-  if (warp < 4) {
-    regs_dec<REGS_FEW>();
-    if (warp == 0) {
-      // ---------------- producer ----------------
-      // inject_stall (test hook): nothing is loaded, so the bounded wait of the next role runs out.
-      if (lane == 0 && !A.inject_stall) {
-        int stage = 0;
-        uint32_t phase = 0;
-        uint32_t issued[STAGES] = {0, 0, 0, 0};
-        bool ok = true;
-        const uint32_t e_bytes = static_cast<uint32_t>(A.e_rows) * KB_BYTES;
-        const uint32_t box_bytes = static_cast<uint32_t>(A.box_c) * KB_BYTES;
-        for_tiles(A.split, A.V, blockIdx.x, [&](const HeadTile& t) {
-          const int nbox = (t.ncol + A.box_c - 1) / A.box_c;
-          for (int kb = 0; kb < num_kb; ++kb) {
-            if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) return ok = false;
-            const uint32_t dst = smem_u32(base + stage * STAGE_BYTES);
-            mbar_arrive_expect_tx(full_bar(stage), e_bytes + static_cast<uint32_t>(nbox) * box_bytes);
-            tma_load_2d(dst, &tmE, full_bar(stage), kb * KE, t.b * BM);
-            for (int j = 0; j < nbox; ++j)
-              tma_load_2d(dst + A_BYTES + static_cast<uint32_t>(j) * box_bytes, &tmC, full_bar(stage), kb * KE,
-                          t.col + j * A.box_c);
-            ++issued[stage];
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          }
-          return true;
-        });
-        if (!ok) {  // every load already issued lands before the block can exit
-          for (int s = 0; s < STAGES; ++s)
-            if (issued[s]) mbar_wait_drain(full_bar(s), (issued[s] - 1u) & 1u, 200000000ull);
-        }
-      }
-    } else if (warp == 1) {
-      // ---------------- MMA issuer ----------------
-      if (lane == 0) {
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool ok = true, issued_any = false;
-        for_tiles(A.split, A.V, blockIdx.x, [&](const HeadTile& t) {
-          const uint32_t idesc = idesc_n(I8, (t.ncol + A.box_c - 1) / A.box_c * A.box_c);
-          for (int k0 = 0; k0 < num_kb; k0 += A.kb_chunk) {
-            if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, wc)) return ok = false;
-            tc_fence_after();
-            const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
-            const int k1 = min(num_kb, k0 + A.kb_chunk);
-            for (int kb = k0; kb < k1; ++kb) {
-              if (!mbar_wait(full_bar(stage), phase, wc)) return ok = false;
-              tc_fence_after();
-              const uint32_t a0 = smem_u32(base + stage * STAGE_BYTES);
-#pragma unroll
-              for (int k = 0; k < KB_BYTES / 32; ++k) {  // 32 bytes of K an instruction
-                const uint64_t da = sdesc_sw128(a0 + 32u * k, 16, 1024);
-                const uint64_t db = sdesc_sw128(a0 + A_BYTES + 32u * k, 16, 1024);
-                const uint32_t add = kb != k0 || k != 0 ? 1u : 0u;
-                if (I8) tc_mma_i8(d, da, db, idesc, add);
-                else tc_mma_bf16(d, da, db, idesc, add);
-              }
-              issued_any = true;
-              tc_commit(empty_bar(stage));
-              if (++stage == STAGES) {
-                stage = 0;
-                phase ^= 1u;
-              }
-            }
-            tc_commit(tfull_bar(acc));
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
-          }
-          return true;
-        });
-        if (!ok && issued_any) {  // no MMA may still write tensor memory when it is released
-          tc_commit(drain_bar);
-          mbar_wait_drain(drain_bar, 0, 200000000ull);
-        }
-      }
-    }
-  } else {
+  if (warp < 4) regs_dec<REGS_FEW>();
+  else regs_inc<REGS_MANY>();
+  if (warp >= 4) {
     // ---------------- epilogue ----------------
-    regs_inc<REGS_MANY>();
-    const int q = warp & 3;            // tensor-memory lanes of this warp
-    const int half = (warp - 4) >> 2;  // columns 128 half .. 128 half + 127 of a tile
-    const uint32_t tquarter = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * 128);
-    uint8_t* mine = scratch + (warp - 4) * SCRATCH_WARP;
-    int* tok_s = reinterpret_cast<int*>(mine);  // [K][32]: the tokens of this warp's rows, -1 for none
+    const int q = warp & 3;             // tensor-memory lanes of this warp
+    const int part = (warp - 4) >> 2;   // columns COLS part .. COLS part + COLS - 1 of a tile
+    const uint32_t tmine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(part * COLS);
     int acc = 0;
     uint32_t acc_phase = 0;
     const float sc = A.inv_t * kLog2e;
     float m = -INFINITY, s = 0.f, w = 0.f;
-    unsigned long long list[L > 0 ? L : 1];
-    float a[128];
-    for_tiles(A.split, A.V, blockIdx.x, [&](const HeadTile& t) {
-      const int r = t.b * BM + q * 32 + lane;
-      const bool rows = t.b * BM + q * 32 < A.N;  // any row of this warp
-      const int ncol = min(128, t.ncol - half * 128);  // columns of this warp (none if <= 0)
-      const int col0 = t.col + half * 128;
+    int tok0 = -1;  // the row's first given token, -1 for none
+    for_tiles(A.split, A.V, [&](const HeadTile& t) {
+      const int row0 = t.b * BM + q * 32, r = row0 + lane;
+      const bool rows = row0 < A.N;                // any row of this warp
+      const int ncol = min(COLS, t.ncol - part * COLS);  // columns of this warp (none if <= 0)
+      const int col0 = t.col + part * COLS;
       if (!OUT && t.first) {
         m = -INFINITY;
         s = w = 0.f;
-        if constexpr (L > 0) {
-#pragma unroll
-          for (int j = 0; j < L; ++j) list[j] = 0;
+        if (A.K == 1) {
+          const int64_t id = r < A.N ? A.tokens[r] : -1;
+          tok0 = id != A.ignore_index && id >= 0 && id < A.V ? static_cast<int>(id) : -1;
         }
-        __syncwarp();
-        for (int k = 0; k < A.K; ++k) {
-          const int64_t id = r < A.N ? A.tokens[static_cast<int64_t>(r) * A.K + k] : -1;
-          tok_s[k * 32 + lane] = id != A.ignore_index && id >= 0 && id < A.V ? static_cast<int>(id) : -1;
-        }
-        __syncwarp();
       }
+      float a[COLS];
+      // columns past ncol hold what an earlier tile left; they are masked below
       for (int k0 = 0; k0 < num_kb; k0 += A.kb_chunk) {
         const bool got = mbar_wait(tfull_bar(acc), acc_phase, wc);
         if (!__all_sync(0xffffffffu, got ? 1 : 0)) return false;
         tc_fence_after();
-        if (rows && ncol > 0) {
-          const uint32_t src = tquarter + static_cast<uint32_t>(acc * BN);
+        const uint32_t src = tmine + static_cast<uint32_t>(acc * BN);
+        if (k0 == 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (32 * j < ncol) {
+          for (int j = 0; j < COLS; j += 16) tmem_ld16(src + j, a + j);
+        } else {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float v[16];
-                tmem_ld16(src + 32u * j + 16u * h, v);
+          for (int j = 0; j < COLS; j += 16) {
+            float v[16];
+            tmem_ld16(src + j, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const int n = 32 * j + 16 * h + i;
-                  if (I8) a[n] = static_cast<float>(__float_as_int(v[i]));
-                  else a[n] = k0 == 0 ? v[i] : a[n] + v[i];
-                }
-              }
-            }
+            for (int i = 0; i < 16; ++i) a[j + i] += v[i];
           }
         }
         tc_fence_before();
-        mbar_arrive(tempty_bar(acc));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(acc));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
       if (!rows) return true;
       if (ncol > 0) {
-        const float es = I8 && r < A.N ? A.e_scale[r] : 0.f;
+        if (I8) {
+          const float es = r < A.N ? A.e_scale[r] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (32 * j >= ncol) {
+          for (int j = 0; j < COLS; ++j) a[j] = static_cast<float>(__float_as_int(a[j]));
 #pragma unroll
-            for (int i = 0; i < 32; ++i) a[32 * j + i] = -INFINITY;
-            continue;
+          for (int j = 0; j < COLS; j += 4) {
+            float4 c = make_float4(0.f, 0.f, 0.f, 0.f);  // the scales' tail is read one by one
+            if (col0 + j + 4 <= A.V) {
+              c = *reinterpret_cast<const float4*>(A.c_scale + col0 + j);
+            } else {
+              if (col0 + j < A.V) c.x = A.c_scale[col0 + j];
+              if (col0 + j + 1 < A.V) c.y = A.c_scale[col0 + j + 1];
+              if (col0 + j + 2 < A.V) c.z = A.c_scale[col0 + j + 2];
+            }
+            a[j] *= es * c.x;
+            a[j + 1] *= es * c.y;
+            a[j + 2] *= es * c.z;
+            a[j + 3] *= es * c.w;
           }
-          float v[32];
-          if (I8) {
-            load_scale32(v, A.c_scale, col0 + 32 * j, A.V);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = a[32 * j + i] * (es * v[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = a[32 * j + i];
-          }
-          if (A.bias != nullptr) add_bias32(v, A.bias, col0 + 32 * j, A.V);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) a[32 * j + i] = 32 * j + i < ncol ? v[i] : -INFINITY;
         }
-        if constexpr (OUT) {
-          // 32 rows x 32 columns at a time through the warp's scratch, then whole rows of it: 32 lanes write one
-          // row's 32 columns, whatever the alignment of V.
-          float* st = reinterpret_cast<float*>(mine);
-          const int n_rows = min(32, A.N - (t.b * BM + q * 32));
-          const int64_t row0 = static_cast<int64_t>(t.b) * BM + q * 32;
+        if (A.bias != nullptr) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (32 * j >= ncol) break;
-            __syncwarp();
+          for (int j = 0; j < COLS; j += 8) {
+            if (col0 + j + 8 <= A.V) {
+              const uint4 u = ld_global_nc_v4(A.bias + col0 + j);
+              const uint32_t us[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) st[lane * 32 + ((i + lane) & 31)] = a[32 * j + i];
-            __syncwarp();
-            const bool in = 32 * j + lane < ncol;
-            for (int k = 0; k < n_rows; ++k) {
-              const float v = st[k * 32 + ((lane + k) & 31)];
-              const int64_t o = (row0 + k) * A.V + col0 + 32 * j + lane;
-              if (in) {
-                if (A.out_fp32) static_cast<float*>(A.out)[o] = v;
-                else static_cast<__nv_bfloat16*>(A.out)[o] = __float2bfloat16_rn(v);
+              for (int k = 0; k < 4; ++k) {
+                a[j + 2 * k] += __uint_as_float(us[k] << 16);
+                a[j + 2 * k + 1] += __uint_as_float(us[k] & 0xffff0000u);
               }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (col0 + j + k < A.V) a[j + k] += __bfloat162float(A.bias[col0 + j + k]);
             }
           }
+        }
+        if constexpr (OUT) {
+          write_logits(A, a, row0, col0, ncol, lane, scratch + (warp - 4) * SCRATCH_WARP);
         } else {
+          const bool cut = ncol < COLS;
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < COLS; ++i) a[i] = i < ncol ? a[i] : -INFINITY;
+          }
           // the given tokens of the row among these columns
           for (int k = 0; k < A.K; ++k) {
-            const int id = tok_s[k * 32 + lane];
+            const int id = A.K == 1 ? tok0 : (r < A.N ? A.tok_t[static_cast<int64_t>(k) * A.N + r] : -1);
             const int at = id - col0;
             const bool hit = id >= 0 && at >= 0 && at < ncol;
-            if (!__any_sync(0xffffffffu, hit)) continue;
+            if (__any_sync(0xffffffffu, hit)) {
+              float z = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const bool here = hit && (at >> 5) == j;
-              if (__any_sync(0xffffffffu, here)) {
-                const float z = pick32(a + 32 * j, at & 31);
-                if (here) A.zt[static_cast<int64_t>(k) * A.N + r] = z;
-              }
+              for (int i = 0; i < COLS; ++i) z = i == at ? a[i] : z;
+              if (hit) A.zt[static_cast<int64_t>(k) * A.N + r] = z;
             }
           }
           float cm[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float x = a[32 * j];
+            float x = a[kHeadPick * j];
 #pragma unroll
-            for (int i = 1; i < 32; ++i) x = fmaxf(x, a[32 * j + i]);
+            for (int i = 1; i < kHeadPick; ++i) x = fmaxf(x, a[kHeadPick * j + i]);
             cm[j] = x;
           }
-          if (A.tile_max != nullptr && r < A.N) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (64 * j < ncol)
-                A.tile_max[static_cast<int64_t>((col0 >> 6) + j) * A.N + r] = fmaxf(cm[2 * j], cm[2 * j + 1]) * A.inv_t;
-            }
-          }
           const float mt = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
+          if (r < A.N) {
+            if (A.tile_max != nullptr) A.tile_max[static_cast<int64_t>(col0 / kSubTile) * A.N + r] = mt * A.inv_t;
+            if (A.pick_max != nullptr)
+              *reinterpret_cast<float4*>(A.pick_max + static_cast<int64_t>(r) * A.picks + col0 / kHeadPick) =
+                  make_float4(cm[0], cm[1], cm[2], cm[3]);
+          }
           const float mn = fmaxf(m, mt);
           if (mn == -INFINITY) {  // nothing but -inf (masked columns) so far; a NaN among them still counts
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
+            for (int i = 0; i < COLS; ++i)
               if (a[i] != a[i]) s = a[i];
           } else {
             if (m != mn && m != -INFINITY) {
@@ -479,67 +469,100 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               s *= f;
             }
             m = mn;
-            float s0 = 0.f, s1 = 0.f, w0 = 0.f, w1 = 0.f;
-#pragma unroll
-            for (int i = 0; i < 128; i += 2) {
-              // below -1e4 (a masked column: -inf) the power is 0, and so is its product with d
-              const float d0 = max_nan((a[i] - mn) * sc, -1e4f), d1 = max_nan((a[i + 1] - mn) * sc, -1e4f);
-              const float e0 = ex2(d0), e1 = ex2(d1);
-              s0 += e0;
-              s1 += e1;
-              w0 = fmaf(d0, e0, w0);
-              w1 = fmaf(d1, e1, w1);
-            }
-            s += s0 + s1;
-            w += w0 + w1;
-          }
-          if constexpr (L > 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // no key of these 32 columns is above that of their largest logit at their first column
-              const uint32_t cj = static_cast<uint32_t>(col0 + 32 * j);
-              if (32 * j >= ncol || !__any_sync(0xffffffffu, make_key(cm[j], cj) > list[L - 1])) continue;
-              const float low = key_value(list[L - 1]);
-              uint32_t bits = 0;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) bits |= (a[32 * j + i] >= low ? 1u : 0u) << i;
-              const int left = ncol - 32 * j;
-              if (left < 32) bits &= (1u << left) - 1u;
-              while (__any_sync(0xffffffffu, bits != 0)) {
-                const int i = __ffs(bits) - 1;  // -1 where this lane has none left
-                unsigned long long x = 0;
-                if (i >= 0) x = make_key(pick32(a + 32 * j, i), cj + static_cast<uint32_t>(i));
-                bits &= bits - 1;
-                if (!__any_sync(0xffffffffu, x > list[L - 1])) continue;
-#pragma unroll
-                for (int k = 0; k < L; ++k) {  // the list stays sorted; what falls out at the end is dropped
-                  const unsigned long long y = list[k];
-                  const bool up = x > y;
-                  list[k] = up ? x : y;
-                  x = up ? y : x;
-                }
-              }
-            }
+            if (cut || A.bias != nullptr) add_powers<true>(a, m, sc, s, w);
+            else add_powers<false>(a, m, sc, s, w);
           }
         }
       }
       if (!OUT && t.last && r < A.N) {
-        const int64_t o = static_cast<int64_t>(2 * t.seg + half) * A.N + r;
+        const int64_t o = static_cast<int64_t>(kHeadParts * t.seg + part) * A.N + r;
         A.part_m[o] = m;
         A.part_s[o] = s;
         A.part_w[o] = w;
-        if constexpr (L > 0) {
-          ulonglong2* dst = reinterpret_cast<ulonglong2*>(A.lists + o * L);
-#pragma unroll
-          for (int k = 0; k < L; k += 2) dst[k / 2] = make_ulonglong2(list[k], list[k + 1]);
-        }
       }
       return true;
     });
+  } else if (warp == 0) {
+    // ---------------- producer ----------------
+    // inject_stall (test hook): nothing is loaded, so the bounded wait of the next role runs out.
+    if (lane == 0 && !A.inject_stall) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued[STAGES] = {0, 0, 0, 0};
+      bool ok = true;
+      const uint32_t e_bytes = static_cast<uint32_t>(A.e_rows) * KB_BYTES;
+      const uint32_t box_bytes = static_cast<uint32_t>(A.box_c) * KB_BYTES;
+      for_tiles(A.split, A.V, [&](const HeadTile& t) {
+        const int nbox = (t.ncol + A.box_c - 1) / A.box_c;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) return ok = false;
+          const uint32_t dst = smem_u32(base + stage * STAGE_BYTES);
+          mbar_arrive_expect_tx(full_bar(stage), e_bytes + static_cast<uint32_t>(nbox) * box_bytes);
+          tma_load_2d(dst, &tmE, full_bar(stage), kb * KE, t.b * BM);
+          for (int j = 0; j < nbox; ++j)
+            tma_load_2d(dst + A_BYTES + static_cast<uint32_t>(j) * box_bytes, &tmC, full_bar(stage), kb * KE,
+                        t.col + j * A.box_c);
+          ++issued[stage];
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        return true;
+      });
+      if (!ok) {  // every load already issued lands before the block can exit
+        for (int s = 0; s < STAGES; ++s)
+          if (issued[s]) mbar_wait_drain(full_bar(s), (issued[s] - 1u) & 1u, 200000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true, issued_any = false;
+      for_tiles(A.split, A.V, [&](const HeadTile& t) {
+        const uint32_t idesc = idesc_n(I8, (t.ncol + A.box_c - 1) / A.box_c * A.box_c);
+        for (int k0 = 0; k0 < num_kb; k0 += A.kb_chunk) {
+          if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, wc)) return ok = false;
+          tc_fence_after();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+          const int k1 = min(num_kb, k0 + A.kb_chunk);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(full_bar(stage), phase, wc)) return ok = false;
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(base + stage * STAGE_BYTES);
+#pragma unroll
+            for (int k = 0; k < KB_BYTES / 32; ++k) {  // 32 bytes of K an instruction
+              const uint64_t da = sdesc_sw128(a0 + 32u * k, 16, 1024);
+              const uint64_t db = sdesc_sw128(a0 + A_BYTES + 32u * k, 16, 1024);
+              const uint32_t add = kb != k0 || k != 0 ? 1u : 0u;
+              if (I8) tc_mma_i8(d, da, db, idesc, add);
+              else tc_mma_bf16(d, da, db, idesc, add);
+            }
+            issued_any = true;
+            tc_commit(empty_bar(stage));
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          tc_commit(tfull_bar(acc));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+        return true;
+      });
+      if (!ok && issued_any) {  // no MMA may still write tensor memory when it is released
+        tc_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0, 200000000ull);
+      }
+    }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) *A.failed = 1;  // what follows then writes NaN
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -553,15 +576,6 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
   return v;
 }
 
-__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = u > v ? u : v;
-  }
-  return v;
-}
-
 // The logit of row r at column `col` in 64 bits, by the whole warp: products of bf16 pairs and of 8-bit pairs are
 // exact, and the order of the sum depends on D alone.
 __device__ double exact_logit(const HeadFinish& F, int64_t r, int col, int lane) {
@@ -570,6 +584,7 @@ __device__ double exact_logit(const HeadFinish& F, int64_t r, int col, int lane)
     long long acc = 0;
     const int8_t* e = F.E8 + r * F.D;
     const int8_t* c = F.C8 + static_cast<int64_t>(col) * F.D;
+#pragma unroll 4
     for (int d = lane * 16; d < F.D; d += 512) {  // D is a multiple of 16
       const uint4 x = *reinterpret_cast<const uint4*>(e + d), y = *reinterpret_cast<const uint4*>(c + d);
       int p = __dp4a(static_cast<int>(x.x), static_cast<int>(y.x), 0);
@@ -583,6 +598,7 @@ __device__ double exact_logit(const HeadFinish& F, int64_t r, int col, int lane)
     double acc = 0.0;
     const __nv_bfloat16* e = F.E + r * F.D;
     const __nv_bfloat16* c = F.C + static_cast<int64_t>(col) * F.D;
+#pragma unroll 8
     for (int d = lane * 8; d < F.D; d += 256) {  // D is a multiple of 8
       const uint4 x = *reinterpret_cast<const uint4*>(e + d), y = *reinterpret_cast<const uint4*>(c + d);
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -600,20 +616,343 @@ __device__ double exact_logit(const HeadFinish& F, int64_t r, int col, int lane)
   return z;
 }
 
-constexpr int kFinishWarps = 4;
-constexpr int kListsLane = 10;  // lists of a row a lane follows: 32 x 10 >= 2 x (148 + 1)
+// ---------------------------------------------------------------------------------------------
+// Alternatives. The head kernel leaves, per row, the largest logit of every pick (16 columns). The best W
+// logits of a row lie in the W picks with the largest maxima (each pick ahead of theirs holds a better one),
+// so W = top_k + 8 picks a row are computed again, and the best of their 16 W logits are the row's. Keeping
+// sorted lists in the head kernel instead costs it more than the products: 2048 x 2048 x 128256, 20
+// alternatives: 1566 us with lists of 28 in registers, against 844 us without.
+//   head_pick_kernel     the W picks of each row; how many rows want each pick
+//   head_scatter_kernel  the rows of each pick, side by side
+//   head_dots_kernel     the logits of each pick for its rows: a pick's 16 rows of C are read once for up to
+//                        64 rows of E
+//   head_finish_kernel   the best of a row's 16 W logits, in order
+// ---------------------------------------------------------------------------------------------
 
-// One warp per row: the segments' statistics joined, then the row's outputs. The alternatives: the heads of the
-// segments' sorted lists are merged, largest key first, into the L > top_k best. The logits behind their
-// keys carry the rounding of 32-bit sums, so where two neighbours are closer than that, their order (and which of
-// them is the top_k-th) is not known yet: every run of such neighbours is computed again in 64 bits and ordered by
-// that, the lower id first among equal ones. Runs are short and rare (a few percent of the neighbours), so this
-// reads little.
-__global__ void __launch_bounds__(kFinishWarps * 32) head_finish_kernel(const __grid_constant__ HeadFinish F) {
+// The want-th largest of a warp's 32 R keys (R in each lane's registers; 0 is below every key), or the smallest of
+// them that is not 0 where there are fewer: bisection on the keys' bits, stopped as soon as a bound has exactly
+// `want` keys at or above it. Each step is R comparisons and one sum over the warp, independent of the data's order
+// (inserting into a sorted list across the lanes takes a chain of shuffles for every key that passes).
+template <int R>
+__device__ __forceinline__ unsigned long long warp_bound(const unsigned long long (&key)[R], int want) {
+  uint32_t hi = 0, lo = 0xffffffffu;  // upper words: of the largest key, and of the smallest that is not 0
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const uint32_t u = static_cast<uint32_t>(key[i] >> 32);
+    hi = max(hi, u);
+    if (key[i] != 0) lo = min(lo, u);
+  }
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (hi == 0) return 1;  // no key at all
+  // upper words first: at least `want` keys are >= lo << 32 (or all that there are), fewer are >= (hi + 1) << 32
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2 + 1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) n += static_cast<uint32_t>(key[i] >> 32) >= mid ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n == want) return static_cast<unsigned long long>(mid) << 32;
+    if (n > want) lo = mid;
+    else hi = mid - 1;
+  }
+  // equal upper words around the bound: the lower ones decide
+  int above = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) above += static_cast<uint32_t>(key[i] >> 32) > lo ? 1 : 0;
+  above = __reduce_add_sync(0xffffffffu, above);
+  uint32_t l = 0, h = 0xffffffffu;
+  while (l < h) {
+    const uint32_t mid = l + (h - l) / 2 + 1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      n += static_cast<uint32_t>(key[i] >> 32) == lo && static_cast<uint32_t>(key[i]) >= mid ? 1 : 0;
+    n = above + __reduce_add_sync(0xffffffffu, n);
+    if (n == want) {
+      l = mid;
+      break;
+    }
+    if (n > want) l = mid;
+    else h = mid - 1;
+  }
+  return (static_cast<unsigned long long>(lo) << 32) | l;
+}
+
+// Writes the warp's keys >= bound (and not 0) to out[0 ..], at most 32; returns how many.
+template <int R>
+__device__ __forceinline__ int warp_collect(const unsigned long long (&key)[R], unsigned long long bound, int lane,
+                                            unsigned long long* out) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const bool in = key[i] != 0 && key[i] >= bound;
+    const unsigned mask = __ballot_sync(0xffffffffu, in);
+    const int at = n + __popc(mask & ((1u << lane) - 1u));
+    if (in && at < 32) out[at] = key[i];
+    n += __popc(mask);
+  }
+  return min(n, 32);
+}
+
+// Sorts a key of each lane: lane 0 gets the largest.
+__device__ __forceinline__ unsigned long long warp_sort(unsigned long long key, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, j);
+      const bool keep_max = ((lane & k) == 0) == ((lane & j) == 0);
+      key = (key > other) == keep_max ? key : other;
+    }
+  }
+  return key;
+}
+
+constexpr int kPickWarpsMax = 32;
+constexpr int kPickHeld = 16;  // maxima a lane holds at a time
+
+// One block per row. Every warp takes its share of the maxima, 512 at a time: the best W of those and of what it
+// kept before. The best W of what the warps kept are the row's picks.
+// The last block to finish lays out the picks' rows: every pick that some row wants gets its place in `rows` and
+// one work item for each 64 of its rows (in any order: nothing depends on it); with few rows it also does the
+// work of head_scatter_kernel.
+__global__ void __launch_bounds__(kPickWarpsMax * 32) head_pick_kernel(const __grid_constant__ HeadPicks P) {
+  __shared__ unsigned long long kept[kPickWarpsMax][32];
+  __shared__ int last;
+  __shared__ int placed[2];  // rows and work items so far
+  if (threadIdx.x < 2) placed[threadIdx.x] = 0;
   wait_for_previous_grid();
-  const int lane = threadIdx.x & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kFinishWarps + (threadIdx.x >> 5);
-  if (r >= F.N) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int r = blockIdx.x, W = P.wanted;
+  const int n = (P.V + kHeadPick - 1) / kHeadPick;
+  const float* mx = P.pick_max + static_cast<int64_t>(r) * P.picks;
+  const int share = (n + nw * 32 - 1) / (nw * 32) * 32;
+  const int u1 = min(n, (w + 1) * share);
+  unsigned long long mine = 0;  // lane i: a key that the warp has kept
+  for (int u0 = w * share; u0 < u1; u0 += 32 * kPickHeld) {
+    unsigned long long key[kPickHeld + 1];
+    float v[kPickHeld];
+#pragma unroll
+    for (int j = 0; j < kPickHeld; ++j) v[j] = u0 + 32 * j + lane < u1 ? mx[u0 + 32 * j + lane] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kPickHeld; ++j) {
+      const int u = u0 + 32 * j + lane;
+      key[j] = u < u1 ? make_key(v[j], static_cast<uint32_t>(u)) : 0ull;
+    }
+    key[kPickHeld] = mine;
+    const unsigned long long bound = warp_bound(key, W);
+    const int m = warp_collect(key, bound, lane, kept[w]);
+    __syncwarp();
+    mine = lane < min(m, W) ? kept[w][lane] : 0ull;
+    __syncwarp();
+  }
+  kept[w][lane] = mine;
+  __syncthreads();
+  if (w == 0) {
+    unsigned long long key[kPickWarpsMax];
+#pragma unroll
+    for (int i = 0; i < kPickWarpsMax; ++i) key[i] = i < nw ? kept[i][lane] : 0ull;
+    const unsigned long long bound = warp_bound(key, W);
+    __syncwarp();
+    const int m = min(W, warp_collect(key, bound, lane, kept[0]));
+    __syncwarp();
+    int unit = -1, slot = 0;
+    if (lane < m) {
+      unit = key_column(kept[0][lane]);
+      slot = atomicAdd(P.count + unit, 1);
+    }
+    P.pick[static_cast<int64_t>(r) * 32 + lane] = unit;
+    P.slot[static_cast<int64_t>(r) * 32 + lane] = slot;
+    __threadfence();
+    __syncwarp();
+    if (lane == 0) last = atomicAdd(P.done, 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // by picks, or, with few rows, by the pairs (row, pick) that came first to their pick
+  const bool by_pair = P.N * 32 < n;
+  const int limit = by_pair ? P.N * 32 : n;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < limit; i += blockDim.x) {
+    int u = i;
+    if (by_pair) u = __ldcg(P.slot + i) == 0 ? __ldcg(P.pick + i) : -1;
+    const int c = u >= 0 ? __ldcg(P.count + u) : 0;
+    if (c == 0) continue;
+    const int items = (c + kHeadDotRows - 1) / kHeadDotRows;
+    const int at = atomicAdd(&placed[0], c), it = atomicAdd(&placed[1], items);
+    P.base[u] = at;
+    for (int k = 0; k < items; ++k)
+      P.items[it + k] = make_int3(u, at + k * kHeadDotRows, min(kHeadDotRows, c - k * kHeadDotRows));
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) P.done[1] = placed[1];
+  if (P.scatter_here) {
+    for (int p = threadIdx.x; p < P.N * 32; p += blockDim.x) {
+      const int u = __ldcg(P.pick + p);
+      if (u >= 0) P.rows[P.base[u] + __ldcg(P.slot + p)] = p;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) head_scatter_kernel(const __grid_constant__ HeadPicks P) {
+  wait_for_previous_grid();
+  const int p = blockIdx.x * 256 + threadIdx.x;
+  if (p >= P.N * 32) return;
+  const int u = P.pick[p];
+  if (u >= 0) P.rows[P.base[u] + P.slot[p]] = p;
+}
+
+__device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16x8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A work item: 16 columns x up to 64 gathered rows. The operands are the rows themselves, read 64 bytes a row and
+// step: the eight warps take every eighth step and their sums are added through shared memory. A lane's 16 bytes
+// of a row feed two instructions whose K positions are the same bytes of both operands, so nothing is rearranged.
+// Rows picked by index suit neither a TMA box nor an M = 128 tile (a pick has 7 rows of 2048 on average); the warp
+// instruction's 16-row tile wastes little, and the kernel is bound by reading C once.
+constexpr int kDotWarps = 8;
+constexpr int kDotStep = 64;  // bytes of a row a step
+// Steps summed in one accumulator: 512 values a warp and part (see the head of the file).
+constexpr int kDotPart = 512 * 2 / kDotStep * kDotWarps;
+
+template <bool I8, int TILES, int UNROLL, typename Acc>
+__device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, const int* ids,
+                                         Acc (*red)[kHeadDotRows * kHeadPick], int64_t pitch, int lane, int w) {
+  const int g = lane >> 2, t = lane & 3;
+  const int steps = static_cast<int>((pitch + kDotStep - 1) / kDotStep);
+  const char* er[TILES][2];
+#pragma unroll
+  for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      er[mt][h] = static_cast<const char*>(P.E) + (ids[min(16 * mt + 8 * h + g, n - 1)] >> 5) * pitch + t * 16;
+  const char* cr[2];
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+    cr[nt] = static_cast<const char*>(P.C) + min(pick * kHeadPick + 8 * nt + g, P.V - 1) * pitch + t * 16;
+  Acc sum[TILES][2][4] = {};
+  for (int s0 = 0; s0 < steps; s0 += kDotPart) {
+    Acc acc[TILES][2][4] = {};
+    const int s1 = min(steps, s0 + kDotPart);
+    for (int s = s0 + w; s < s1; s += kDotWarps * UNROLL) {
+      uint4 b[UNROLL][2], a[UNROLL][TILES][2];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int64_t off = static_cast<int64_t>(s + u * kDotWarps) * kDotStep;
+        const bool in = s + u * kDotWarps < s1 && off + t * 16 < pitch;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) b[u][nt] = in ? ld_global_nc_v4(cr[nt] + off) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            a[u][mt][h] = in ? ld_global_nc_v4(er[mt][h] + off) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+        for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const uint4 x = a[u][mt][0], y = a[u][mt][1];
+            mma_16x8(acc[mt][nt], x.x, y.x, x.y, y.y, b[u][nt].x, b[u][nt].y);
+            mma_16x8(acc[mt][nt], x.z, y.z, x.w, y.w, b[u][nt].z, b[u][nt].w);
+          }
+    }
+#pragma unroll
+    for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[mt][nt][i] += acc[mt][nt][i];
+  }
+#pragma unroll
+  for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[w][(16 * mt + g + 8 * (i >> 1)) * kHeadPick + 8 * nt + 2 * t + (i & 1)] = sum[mt][nt][i];
+}
+
+template <bool I8>
+__global__ void __launch_bounds__(kDotWarps * 32, 2) head_dots_kernel(const __grid_constant__ HeadPicks P) {
+  using Acc = typename std::conditional<I8, int, float>::type;
+  __shared__ Acc red[kDotWarps][kHeadDotRows * kHeadPick];
+  __shared__ int ids[kHeadDotRows];
+  wait_for_previous_grid();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t pitch = static_cast<int64_t>(P.D) * (I8 ? 1 : 2);  // a multiple of 16 bytes
+  const int nitems = P.done[1];
+  for (int it = blockIdx.x; it < nitems; it += gridDim.x) {
+    const int3 item = P.items[it];
+    __syncthreads();  // the previous item's sums and ids have been read
+    if (threadIdx.x < item.z) ids[threadIdx.x] = P.rows[item.y + threadIdx.x];
+    __syncthreads();
+    if (item.z <= 16) dot_item<I8, 1, 4>(P, item.x, item.z, ids, red, pitch, lane, w);
+    else dot_item<I8, 4, 1>(P, item.x, item.z, ids, red, pitch, lane, w);
+    __syncthreads();
+    for (int i = threadIdx.x; i < item.z * kHeadPick; i += kDotWarps * 32) {
+      Acc z = 0;
+#pragma unroll
+      for (int k = 0; k < kDotWarps; ++k) z += red[k][i];
+      const int p = ids[i / kHeadPick], col = item.x * kHeadPick + i % kHeadPick;
+      if (col < P.V) {
+        float v = static_cast<float>(z);
+        if (I8) v *= P.e_scale[p >> 5] * P.c_scale[col];
+        if (P.bias != nullptr) v += __bfloat162float(P.bias[col]);
+        P.logits[static_cast<int64_t>(p) * kHeadPick + i % kHeadPick] = v;
+      }
+    }
+  }
+}
+
+// The row's softmax statistics from those of its segments: (m, s, w) and (m2, s2, w2) -> (m, s, w) of both.
+__device__ __forceinline__ void join_stats(float& m, float& s, float& w, float m2, float s2, float w2, float sc) {
+  const float mn = fmaxf(m, m2);
+  if (mn == -INFINITY) {  // nothing but masked columns in either: the sums are 0, or NaN
+    s += s2;
+    return;
+  }
+  // a side without a maximum has the sums 0 (or NaN); below -1e4 the power is 0 and so is its product with d
+  const float d = fmaxf((m - mn) * sc, -1e4f), d2 = fmaxf((m2 - mn) * sc, -1e4f);
+  const float f = ex2(d), f2 = ex2(d2);
+  w = f * fmaf(s, d, w) + f2 * fmaf(s2, d2, w2);
+  s = f * s + f2 * s2;
+  m = mn;
+}
+
+// WARPS warps per row, ROWS rows a block: the segments' statistics joined, then the row's outputs.
+// Alternatives: the best 32 of the picks' logits, sorted. They carry the rounding of 32-bit sums, so where two
+// neighbours are closer than that, their order (and which of them is the top_k-th) is not known yet: every run
+// of such neighbours is computed again in 64 bits, a warp for each logit, and ordered by that, the lower id first among
+// equal ones. Runs are short and rare (a few percent of the neighbours), so this reads little.
+template <int WARPS, int ROWS>
+__global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __grid_constant__ HeadFinish F) {
+  __shared__ float stats[WARPS][3];
+  __shared__ unsigned long long best[32];
+  __shared__ double exact[32];
+  __shared__ unsigned run_mask;
+  wait_for_previous_grid();
+  const int lane = threadIdx.x & 31, wi = (threadIdx.x >> 5) % WARPS;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x >> 5) / WARPS;
+  if (r >= F.N) return;  // ROWS > 1 only: there nothing below waits for other warps
   const HeadSplit& S = F.split;
   const int b = static_cast<int>(r / kHeadBM);
   int g = static_cast<int>(static_cast<long long>(b) * S.ngroups / S.nb);  // the group of row block b, or one off
@@ -621,36 +960,43 @@ __global__ void __launch_bounds__(kFinishWarps * 32) head_finish_kernel(const __
   while (S.group_begin(g + 1) <= b) ++g;
   const int b0 = S.group_begin(g), gb = S.group_begin(g + 1) - b0;
   const int total = S.units(gb), P = S.parts(total);
-  const int nlist =
-      2 * (HeadSplit::owner(S.units(b - b0 + 1) - 1, total, P) - HeadSplit::owner(S.units(b - b0), total, P) + 1);
-  const bool failed = *F.err != 0;
+  const int nseg = kHeadParts * (HeadSplit::owner(S.units(b - b0 + 1) - 1, total, P) -
+                                 HeadSplit::owner(S.units(b - b0), total, P) + 1);
+  const bool failed = *F.failed != 0;
   const float sc = F.inv_t * kLog2e;
 
-  float m = -INFINITY;
-  for (int i = lane; i < nlist; i += 32) m = fmaxf(m, F.part_m[static_cast<int64_t>(i) * F.N + r]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float s = 0.f, w = 0.f;
-  for (int i = lane; i < nlist; i += 32) {
+  float m = -INFINITY, s = 0.f, w = 0.f;
+#pragma unroll 4
+  for (int i = wi * 32 + lane; i < nseg; i += 32 * WARPS) {
     const int64_t o = static_cast<int64_t>(i) * F.N + r;
-    const float mi = F.part_m[o], si = F.part_s[o];
-    if (mi == -INFINITY) {
-      s += si;  // 0, or NaN
-    } else {
-      const float d = (mi - m) * sc, f = ex2(d);
-      s = fmaf(f, si, s);
-      w += f * fmaf(si, fmaxf(d, -1e30f), F.part_w[o]);
-    }
+    join_stats(m, s, w, F.part_m[o], F.part_s[o], F.part_w[o], sc);
   }
-  s = warp_sum(s);
-  w = warp_sum(w);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o),
+                w2 = __shfl_xor_sync(0xffffffffu, w, o);
+    join_stats(m, s, w, m2, s2, w2, sc);
+  }
+  if (WARPS > 1) {
+    if (lane == 0) {
+      stats[wi][0] = m;
+      stats[wi][1] = s;
+      stats[wi][2] = w;
+    }
+    __syncthreads();
+    m = stats[0][0];
+    s = stats[0][1];
+    w = stats[0][2];
+#pragma unroll
+    for (int i = 1; i < WARPS; ++i) join_stats(m, s, w, stats[i][0], stats[i][1], stats[i][2], sc);
+  }
   const float ln_s = logf(s);
   const float nan = __int_as_float(0x7fffffff);
   const bool none = m == -INFINITY && s == 0.f;  // every logit of the row is -inf
-  if (F.K > 0) {
+  if (F.K > 0 && wi == 0) {
     bool any = false;
-    for (int k = lane; k < F.K; k += 32) {
-      const int64_t id = F.tokens[r * F.K + k];
+    if (lane < F.K) {
+      const int64_t id = F.tokens[r * F.K + lane];
       float lp = 0.f;
       if (id != F.ignore_index) {
         any = true;
@@ -658,10 +1004,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32) head_finish_kernel(const __
           record_error(F.err, kErrTargetRange);
           lp = nan;
         } else {
-          lp = none ? -INFINITY : (F.zt[static_cast<int64_t>(k) * F.N + r] - m) * F.inv_t - ln_s;
+          lp = none ? -INFINITY : (F.zt[static_cast<int64_t>(lane) * F.N + r] - m) * F.inv_t - ln_s;
         }
       }
-      F.logprobs[r * F.K + k] = failed ? nan : lp;
+      F.logprobs[r * F.K + lane] = failed ? nan : lp;
     }
     any = __any_sync(0xffffffffu, any);
     if (lane == 0) {
@@ -670,74 +1016,83 @@ __global__ void __launch_bounds__(kFinishWarps * 32) head_finish_kernel(const __
       F.lse[r] = failed ? nan : (none ? -INFINITY : fmaf(m, F.inv_t, ln_s));
     }
   }
-  if (F.L == 0) return;
-
-  // merge: lane l follows lists l, l + 32, ...
-  unsigned long long head[kListsLane];
-  int pos[kListsLane];
-  const int64_t step = static_cast<int64_t>(F.N) * F.L;
-#pragma unroll
-  for (int i = 0; i < kListsLane; ++i) {
-    const int li = lane + 32 * i;
-    pos[i] = 0;
-    head[i] = li < nlist ? F.lists[li * step + r * F.L] : 0;
-  }
-  const int want = F.L;
-  unsigned long long mykey = 0;  // lane i: the i-th best
-  for (int j = 0; j < want; ++j) {
-    unsigned long long best = 0;
-#pragma unroll
-    for (int i = 0; i < kListsLane; ++i) best = head[i] > best ? head[i] : best;
-    const unsigned long long top = warp_max_u64(best);
-    if (lane == j) mykey = top;
-    if (top == 0) break;
-    if (best == top) {
-#pragma unroll
-      for (int i = 0; i < kListsLane; ++i) {
-        if (head[i] == top) {
-          ++pos[i];
-          head[i] = pos[i] < F.L ? F.lists[(lane + 32 * i) * step + r * F.L + pos[i]] : 0;
-        }
-      }
+  if (ROWS > 1 || F.top_k == 0) return;
+  if (failed) {
+    if (threadIdx.x < F.top_k) {
+      F.top_logprobs[r * F.top_k + threadIdx.x] = nan;
+      F.top_ids[r * F.top_k + threadIdx.x] = -1;
     }
+    return;
   }
-  const float v = key_value(mykey);
-  const int col = mykey == 0 ? -1 : key_column(mykey);
-  // Neighbours closer than what a 32-bit sum loses: the sums of 512 products carry up to a few 2^-24 of their
-  // largest part each (2^-15 of the logits leaves room); 8-bit products are exact but for three roundings.
-  const float scale = fmaxf(fabsf(__shfl_sync(0xffffffffu, v, 0)), fabsf(v));
-  const float tol = (F.C8 != nullptr ? 0x1p-21f : 0x1p-15f) * (scale < 3e38f ? scale : 0.f);
-  const float before = __shfl_up_sync(0xffffffffu, v, 1);
-  const bool close = lane > 0 && col >= 0 && isfinite(v) && isfinite(before) && before - v <= tol;
-  const unsigned joins = __ballot_sync(0xffffffffu, close);  // bit i: i is close to i - 1
-  const unsigned runs = joins | (joins >> 1);                // members of a run
-  double zx = static_cast<double>(v);
-  for (unsigned todo = runs; todo != 0; todo &= todo - 1) {
+
+  if (wi == 0) {
+    unsigned long long key[kHeadPick];
+#pragma unroll
+    for (int i = 0; i < kHeadPick; ++i) {
+      const int j = 2 * i + (lane >> 4);  // two picks a step
+      const int unit = j < F.wanted ? F.pick[r * 32 + j] : -1;
+      const int c = unit * kHeadPick + (lane & 15);
+      key[i] = unit >= 0 && c < F.V ? make_key(F.logits[(r * 32 + j) * kHeadPick + (lane & 15)], static_cast<uint32_t>(c))
+                                    : 0ull;
+    }
+    const unsigned long long bound = warp_bound(key, 32);
+    best[lane] = 0;
+    __syncwarp();
+    warp_collect(key, bound, lane, best);
+    __syncwarp();
+    const unsigned long long mine = warp_sort(best[lane], lane);
+    best[lane] = mine;
+    const float v = key_value(mine);
+    // Neighbours closer than what a 32-bit sum loses: the sums of 512 products carry up to a few 2^-24 of their
+    // largest part each (2^-15 of the logits leaves room); 8-bit products are exact but for three roundings.
+    const float scale = fmaxf(fabsf(__shfl_sync(0xffffffffu, v, 0)), fabsf(v));
+    const float tol = (F.C8 != nullptr ? 0x1p-21f : 0x1p-15f) * (scale < 3e38f ? scale : 0.f);
+    const float before = __shfl_up_sync(0xffffffffu, v, 1);
+    const bool close = lane > 0 && mine != 0 && isfinite(v) && isfinite(before) && before - v <= tol;
+    const unsigned joins = __ballot_sync(0xffffffffu, close);  // bit i: i is close to i - 1
+    exact[lane] = static_cast<double>(v);
+    if (lane == 0) run_mask = joins;
+  }
+  __syncthreads();
+  const unsigned joins = run_mask, runs = joins | (joins >> 1);  // members of a run
+  int turn = 0;
+  for (unsigned todo = runs; todo != 0; todo &= todo - 1, ++turn) {
+    if (turn % WARPS != wi) continue;
     const int i = __ffs(todo) - 1;
-    const double z = exact_logit(F, r, __shfl_sync(0xffffffffu, col, i), lane);
-    if (lane == i) zx = z;
+    const double z = exact_logit(F, r, key_column(best[i]), lane);
+    if (lane == 0) exact[i] = z;
   }
+  __syncthreads();
+  if (wi != 0) return;
+  const bool in = best[lane] != 0;
+  const int col = in ? key_column(best[lane]) : -1;
+  const double zx = exact[lane];
   int place = lane;
   if ((runs >> lane) & 1u) {
     const unsigned starts = ~joins;  // bit i: a run (or a single one) starts at i
     place = 31 - __clz(static_cast<int>(starts & (0xffffffffu >> (31 - lane))));
+    const int first = place;
+    for (int i = first; i < 32 && (i == first || ((joins >> i) & 1u)); ++i) {
+      const double zi = exact[i];
+      if (i != lane && (zi > zx || (zi == zx && key_column(best[i]) < col))) ++place;
+    }
   }
-  const int first = place;  // start of this lane's run
-  for (int i = 0; i < 32; ++i) {
-    const int fi = __shfl_sync(0xffffffffu, first, i), ci = __shfl_sync(0xffffffffu, col, i);
-    const double zi = __shfl_sync(0xffffffffu, zx, i);
-    if (((runs >> lane) & 1u) && i != lane && ((runs >> i) & 1u) && fi == first && (zi > zx || (zi == zx && ci < col)))
-      ++place;
-  }
-  if (place < F.top_k && col >= 0) {
+  if (place < F.top_k && in) {
     const float lp = m == -INFINITY ? -INFINITY
                                     : static_cast<float>((zx - static_cast<double>(m)) * static_cast<double>(F.inv_t)) - ln_s;
-    F.top_logprobs[r * F.top_k + place] = failed || s != s ? nan : lp;
-    F.top_ids[r * F.top_k + place] = failed ? -1 : col;
-  } else if (col < 0 && lane < F.top_k) {  // NaN logits leave the lists short
-    F.top_logprobs[r * F.top_k + lane] = nan;
-    F.top_ids[r * F.top_k + lane] = -1;
+    F.top_logprobs[r * F.top_k + place] = s != s ? nan : lp;
+    F.top_ids[r * F.top_k + place] = col;
   }
+}
+
+// tokens [N, K] -> tok_t [K, N], -1 for those that ask for nothing: the head kernel's warps read a token of 32 rows
+// at once.
+__global__ void __launch_bounds__(256) head_tokens_kernel(const int64_t* __restrict__ tokens, int N, int K, int V,
+                                                          int64_t ignore_index, int* __restrict__ tok_t) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<int64_t>(N) * K) return;
+  const int64_t id = tokens[i];
+  tok_t[(i % K) * N + i / K] = id != ignore_index && id >= 0 && id < V ? static_cast<int>(id) : -1;
 }
 
 // One block per row: the largest magnitude, then the integers. scale = max |x| / 127, rounded to nearest; q is the
@@ -801,10 +1156,10 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
   }
 }
 
-template <bool I8, int L, bool OUT>
+template <bool I8, bool OUT>
 cudaError_t launch_one(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool after_kernel,
                        cudaStream_t s) {
-  auto kernel = head_kernel<I8, L, OUT>;
+  auto kernel = head_kernel<I8, OUT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if (after_kernel) {
@@ -819,27 +1174,51 @@ cudaError_t launch_one(const CUtensorMap& tmE, const CUtensorMap& tmC, const Hea
 
 }  // namespace
 
-cudaError_t launch_head(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool int8, int list_len,
-                        bool after_kernel, cudaStream_t s) {
-  if (A.out != nullptr) return launch_one<true, 0, true>(tmE, tmC, A, after_kernel, s);
-  if (int8) {
-    if (list_len == 0) return launch_one<true, 0, false>(tmE, tmC, A, after_kernel, s);
-    if (list_len == kHeadShortList) return launch_one<true, kHeadShortList, false>(tmE, tmC, A, after_kernel, s);
-    return launch_one<true, kHeadLongList, false>(tmE, tmC, A, after_kernel, s);
-  }
-  if (list_len == 0) return launch_one<false, 0, false>(tmE, tmC, A, after_kernel, s);
-  if (list_len == kHeadShortList) return launch_one<false, kHeadShortList, false>(tmE, tmC, A, after_kernel, s);
-  return launch_one<false, kHeadLongList, false>(tmE, tmC, A, after_kernel, s);
+cudaError_t launch_head(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool int8, bool after_kernel,
+                        cudaStream_t s) {
+  if (A.out != nullptr) return launch_one<true, true>(tmE, tmC, A, after_kernel, s);
+  if (int8) return launch_one<true, false>(tmE, tmC, A, after_kernel, s);
+  return launch_one<false, false>(tmE, tmC, A, after_kernel, s);
 }
 
-cudaError_t launch_head_finish(const HeadFinish& F, bool after_kernel, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((F.N + kFinishWarps - 1) / kFinishWarps)), block(kFinishWarps * 32);
-  if (after_kernel) {
-    const cudaError_t e = launch_after_previous(head_finish_kernel, grid, block, 0, s, F);
+cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s) {
+  // With few rows each gets more warps: a row's picks are then found in a quarter of the time, at the cost of more
+  // insertions, which only full machines feel.
+  const int warps = P.N < 2 * sms ? kPickWarpsMax : 8;
+  P.scatter_here = P.N <= 128 ? 1 : 0;
+  cudaError_t e = launch_after_previous(head_pick_kernel, dim3(P.N), dim3(32 * warps), 0, s, P);
+  if (e != cudaSuccess) return e;
+  if (!P.scatter_here) {
+    e = launch_after_previous(head_scatter_kernel, dim3((P.N * 32 + 255) / 256), dim3(256), 0, s, P);
     if (e != cudaSuccess) return e;
-  } else {
-    head_finish_kernel<<<grid, block, 0, s>>>(F);
   }
+  const dim3 grid(std::min(P.N * 32, 2 * sms)), block(kDotWarps * 32);
+  e = int8 ? launch_after_previous(head_dots_kernel<true>, grid, block, 0, s, P)
+           : launch_after_previous(head_dots_kernel<false>, grid, block, 0, s, P);
+  note_launches(P.scatter_here ? 2 : 3);
+  return e;
+}
+
+cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s) {
+  // A block of eight warps per row where a row has many segments (few row blocks share the machine), so that they are
+  // read at once; else two where alternatives are to be ordered; else a warp per row, four rows a block.
+  cudaError_t e;
+  if (F.split.max_segments() > 16) {
+    e = launch_after_previous(head_finish_kernel<8, 1>, dim3(F.N), dim3(256), 0, s, F);
+  } else if (F.top_k > 0) {
+    e = launch_after_previous(head_finish_kernel<2, 1>, dim3(F.N), dim3(64), 0, s, F);
+  } else {
+    e = launch_after_previous(head_finish_kernel<1, 4>, dim3((F.N + 3) / 4), dim3(128), 0, s, F);
+  }
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_head_tokens(const int64_t* tokens, int N, int K, int V, int64_t ignore_index, int* tok_t,
+                               cudaStream_t s) {
+  const int64_t n = static_cast<int64_t>(N) * K;
+  head_tokens_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(tokens, N, K, V, ignore_index, tok_t);
   note_launches(1);
   return cudaGetLastError();
 }

@@ -15,20 +15,29 @@ constexpr int kHeadBN = 256;       // vocabulary columns of a logit tile
 constexpr int kHeadGroup = 32;     // row blocks that walk the vocabulary together (their E stays in L2)
 constexpr int kHeadMaxTokens = 32; // given tokens a row
 constexpr int kHeadMaxTop = 24;    // alternatives a row
-constexpr int kHeadShortList = 12; // candidates kept for up to 8 alternatives, and for more: at least 4 to spare,
-constexpr int kHeadLongList = 28;  // see head_finish_kernel
+constexpr int kHeadParts = 4;      // epilogue warps of a row: partial statistics of a segment
+constexpr int kHeadPick = 16;      // columns of a pick: the unit whose largest logit is kept for the alternatives
+constexpr int kHeadDotRows = 64;   // rows of a work item of head_dots_kernel
+constexpr int kHeadSlab = 4096;    // rows whose alternatives are found at a time: bounds their workspace
 
 // How the logit tiles are split over the blocks of the grid. Row blocks are taken in `ngroups` groups of
 // nearly equal size. A group's work is the list of its units (`unit` vocabulary columns of one row
-// block), row block by row block; block c of the P = min(grid, units) that take part gets the units
-// [c U / P, (c + 1) U / P). What a block gets of one row block is a segment: it keeps the softmax
+// block), row block by row block; part c of the P = min(grid, units) parts gets the units
+// [c U / P, (c + 1) U / P), and one block walks it. What a block gets of one row block is a segment: it keeps the softmax
 // statistics (and the best alternatives) of the segment on chip and writes them once.
+constexpr int kHeadMaxGrid = 148;  // SMs of a B200
+
 struct HeadSplit {
   int nb;       // row blocks
   int nu;       // units of a row block
-  int unit;     // columns of a unit: a multiple of 32
+  int unit;     // columns of a unit: a multiple of 64
   int ngroups;
-  int grid;
+  int grid;     // at most kHeadMaxGrid
+  // Which part a block takes, for the smaller groups and for those with one row block more: by where in the
+  // vocabulary the part starts. Neighbouring blocks (two SMs that share a path to L2) then walk the same columns of
+  // C on different row blocks, and what both load at a time crosses from L2 once (2048 x 2048 x 128256: 334
+  // million sectors in the parts' own order, where neighbours share rows of E instead).
+  uint8_t order[2][kHeadMaxGrid];
 
   __host__ __device__ int group_begin(int g) const {
     return static_cast<int>(static_cast<long long>(nb) * g / ngroups);
@@ -38,7 +47,7 @@ struct HeadSplit {
   __host__ __device__ static int part_begin(int c, int total, int P) {
     return static_cast<int>(static_cast<long long>(total) * c / P);
   }
-  // The block that gets unit x: the largest c with part_begin(c) <= x.
+  // The part that holds unit x: the largest c with part_begin(c) <= x.
   __host__ __device__ static int owner(int x, int total, int P) {
     return static_cast<int>(((static_cast<long long>(x) + 1) * P - 1) / total);
   }
@@ -60,20 +69,45 @@ struct HeadArgs {
   const float* e_scale;       // [N], [V]: scales of 8-bit operands
   const float* c_scale;
   const int64_t* tokens;      // [N, K]
+  const int* tok_t;           // [K, N], -1 for none (K > 1)
   int64_t ignore_index;
   int K;
   float* zt;        // [K, N]: logits of the given tokens
   float* tile_max;  // [ceil(V / 64), N]: largest y of each 64 columns, or null
+  float* pick_max;  // [N, picks]: largest logit of each pick, or null
+  int picks;        // a multiple of 4, at least the number of picks
   float inv_t;      // 1 / temperature
-  float* part_m;    // [2 segments, N]: largest logit, sum of exp, sum of (y - largest y) log2 e exp
+  float* part_m;    // [4 segments, N]: largest logit, sum of 2^d, sum of d 2^d, see cce_head.cu
   float* part_s;
   float* part_w;
-  unsigned long long* lists;  // [2 segments, N, L]: best keys, highest first
   void* out;        // [N, V] logits (8-bit product)
   int out_fp32;
   int* err;
+  int* failed;      // set when a bounded wait ran out
   uint64_t timeout_ns;
   int inject_stall;
+};
+
+// The picks of every row, their rows and logits (cce_head.cu: alternatives).
+struct HeadPicks {
+  int N, D, V;
+  const void* E;  // bf16 or 8-bit rows
+  const void* C;
+  const float* e_scale;
+  const float* c_scale;
+  const __nv_bfloat16* bias;
+  const float* pick_max;  // [N, picks]
+  int picks;
+  int wanted;       // picks a row, at most 32
+  int scatter_here;
+  int* done;        // [2]: blocks done (zero before), work items
+  int* count;       // [picks], zero before: rows that want the pick
+  int* base;        // [picks]: their place in rows
+  int* pick;        // [N, 32]: the rows' picks, -1 for none
+  int* slot;        // [N, 32]: place among the pick's rows
+  int* rows;        // [32 N]: 32 row + j
+  int3* items;      // [32 N]: pick, first of its rows, how many
+  float* logits;    // [N, 32, 16]
 };
 
 struct HeadFinish {
@@ -94,8 +128,9 @@ struct HeadFinish {
   const float* part_m;
   const float* part_s;
   const float* part_w;
-  const unsigned long long* lists;
-  int L;  // entries of a list (0: no alternatives)
+  const int* pick;
+  const float* logits;  // of the picks
+  int wanted;
   int top_k;
   float* logprobs;   // [N, K]
   float* entropy;    // [N]
@@ -103,11 +138,16 @@ struct HeadFinish {
   float* top_logprobs;  // [N, top_k]
   int64_t* top_ids;
   int* err;
+  const int* failed;
 };
 
-cudaError_t launch_head(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool int8, int list_len,
-                        bool after_kernel, cudaStream_t s);
-cudaError_t launch_head_finish(const HeadFinish& F, bool after_kernel, cudaStream_t s);
+cudaError_t launch_head(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool int8, bool after_kernel,
+                        cudaStream_t s);
+// These two follow a kernel of the same call on s.
+cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s);
+cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s);
+cudaError_t launch_head_tokens(const int64_t* tokens, int N, int K, int V, int64_t ignore_index, int* tok_t,
+                               cudaStream_t s);
 // Rows of 8-bit integers: scale = max |x| / 127, q = x / scale to the nearest integer.
 cudaError_t launch_quantize_rows(const __nv_bfloat16* x, int64_t rows, int64_t D, int8_t* q, float* scale,
                                  cudaStream_t s);

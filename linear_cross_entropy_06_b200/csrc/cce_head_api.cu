@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
+#include <numeric>
 
 #include "cce.h"
 #include "cce_head.h"
@@ -60,40 +61,58 @@ bool logprobs_ok(const cce_logprob_problem* p, bool set_error) {
 
 // The split of the logit tiles over `sms` blocks. With at least kWideTiles tiles a block, units of a whole tile:
 // one load a stage brings 256 rows of C, and a block's share is uneven by at most one tile in that many. With fewer,
-// units of 32 columns (64 where maxima of 64 columns are kept), loaded 32 rows at a time, so that the blocks' shares
-// of C stay even: one row block on 148 SMs gets 27.1 units of 32 columns (at most 28) instead of 3.4 tiles (at
-// most 4).
+// units of 64 columns, loaded 64 rows at a time, so that the blocks' shares of C stay even: one row block of 128256
+// columns on 148 SMs gets 13.5 units (at most 14) instead of 3.4 tiles (at most 4).
 constexpr int64_t kWideTiles = 12;
 
-cce::HeadSplit make_split(int64_t N, int64_t V, bool maxima, int sms) {
+cce::HeadSplit make_split(int64_t N, int64_t V, int sms) {
   cce::HeadSplit S{};
   S.nb = static_cast<int>(ceil_div(N, cce::kHeadBM));
   S.ngroups = static_cast<int>(ceil_div(S.nb, cce::kHeadGroup));
   S.grid = sms;
   const int64_t rows = std::max<int64_t>(S.nb / std::max(S.ngroups, 1), 1);
-  const bool wide = rows * ceil_div(V, cce::kHeadBN) >= kWideTiles * sms;
-  S.unit = wide ? cce::kHeadBN : (maxima ? 64 : 32);
+  S.unit = rows * ceil_div(V, cce::kHeadBN) >= kWideTiles * sms ? cce::kHeadBN : 64;
   S.nu = static_cast<int>(ceil_div(V, S.unit));
+  for (int k = 0; k < 2; ++k) {
+    const int total = S.units(static_cast<int>(rows) + k), P = S.parts(total);
+    int parts[cce::kHeadMaxGrid];
+    std::iota(parts, parts + P, 0);
+    std::stable_sort(parts, parts + P, [&](int a, int b) {
+      return cce::HeadSplit::part_begin(a, total, P) % S.nu < cce::HeadSplit::part_begin(b, total, P) % S.nu;
+    });
+    for (int i = 0; i < P; ++i) S.order[k][i] = static_cast<uint8_t>(parts[i]);
+  }
   return S;
 }
 
-int list_len(int top_k) {
-  return top_k == 0 ? 0 : top_k <= cce::kHeadShortList - 4 ? cce::kHeadShortList : cce::kHeadLongList;
-}
+constexpr int kMaxSms = cce::kHeadMaxGrid;  // the workspace is sized for it; a device with fewer SMs needs no more
 
-constexpr int kMaxSms = 148;  // the workspace is sized for a B200; a part with fewer SMs needs no more
+int picks_pitch(int64_t V) { return static_cast<int>(ceil_div(ceil_div(V, cce::kHeadPick), 4) * 4); }
+int picks_wanted(int top_k) { return top_k + 8; }
 
 struct HeadWs {
   cce::WsHeader* hdr;
+  int* counters;   // HeadPicks.done and .count, directly behind the header
+  size_t counter_bytes;
+  int* tok_t;      // [K, N] (K > 1)
   float* zt;       // [K, N]
-  float* part_m;   // [2 segments, N] each
+  float* part_m;   // [4 segments, N] each
   float* part_s;
   float* part_w;
-  unsigned long long* lists;  // [2 segments, N, L]
+  float* pick_max; // alternatives, for a slab of rows: see HeadPicks
+  int* base;
+  int* pick;
+  int* slot;
+  int* rows;
+  int3* items;
+  float* logits;
   int8_t* e8;      // [N, D]
   float* e_scale;  // [N]
   size_t bytes;
 };
+
+// The statistics are those of a slab of rows where alternatives are wanted, of all rows where not.
+int64_t slab_rows(int64_t N, int top_k) { return top_k > 0 ? std::min<int64_t>(N, cce::kHeadSlab) : N; }
 
 HeadWs carve(int64_t N, int64_t D, int64_t V, int K, int top_k, bool int8, bool stats, void* base) {
   HeadWs w{};
@@ -104,42 +123,61 @@ HeadWs carve(int64_t N, int64_t D, int64_t V, int K, int top_k, bool int8, bool 
     off = align_up(off + bytes);
     return ptr;
   };
-  const size_t n = static_cast<size_t>(N);
   w.hdr = reinterpret_cast<cce::WsHeader*>(b);
+  const int64_t slab = slab_rows(N, top_k);
+  const size_t n = static_cast<size_t>(slab), k = static_cast<size_t>(K);
+  if (top_k > 0) {
+    const size_t picks = static_cast<size_t>(picks_pitch(V));
+    w.counter_bytes = sizeof(int) * (4 + picks);
+    w.counters = reinterpret_cast<int*>(take(w.counter_bytes));
+    w.base = reinterpret_cast<int*>(take(sizeof(int) * picks));
+    w.pick_max = reinterpret_cast<float*>(take(sizeof(float) * n * picks));
+    w.pick = reinterpret_cast<int*>(take(sizeof(int) * n * 32));
+    w.slot = reinterpret_cast<int*>(take(sizeof(int) * n * 32));
+    w.rows = reinterpret_cast<int*>(take(sizeof(int) * n * 32));
+    w.items = reinterpret_cast<int3*>(take(sizeof(int3) * n * 32));
+    w.logits = reinterpret_cast<float*>(take(sizeof(float) * n * 32 * cce::kHeadPick));
+  }
   if (stats && N > 0) {
-    const cce::HeadSplit S = make_split(N, V, false, kMaxSms);
-    const size_t parts = 2 * static_cast<size_t>(S.max_segments()) * n;
-    w.zt = reinterpret_cast<float*>(take(sizeof(float) * n * static_cast<size_t>(K)));
+    // the largest of the slabs' splits: a slab with fewer row blocks has more segments a row block
+    size_t parts = 0;
+    for (int64_t rows : {slab, N % slab}) {
+      if (rows == 0) continue;
+      const size_t segments = static_cast<size_t>(make_split(rows, V, kMaxSms).max_segments());
+      parts = std::max(parts, cce::kHeadParts * segments * static_cast<size_t>(rows));
+    }
+    if (K > 1) w.tok_t = reinterpret_cast<int*>(take(sizeof(int) * n * k));
+    w.zt = reinterpret_cast<float*>(take(sizeof(float) * n * k));
     w.part_m = reinterpret_cast<float*>(take(sizeof(float) * parts));
     w.part_s = reinterpret_cast<float*>(take(sizeof(float) * parts));
     w.part_w = reinterpret_cast<float*>(take(sizeof(float) * parts));
-    w.lists = reinterpret_cast<unsigned long long*>(take(8 * parts * static_cast<size_t>(list_len(top_k))));
   }
   if (int8) {
-    w.e8 = reinterpret_cast<int8_t*>(take(n * static_cast<size_t>(D)));
-    w.e_scale = reinterpret_cast<float*>(take(sizeof(float) * n));
+    w.e8 = reinterpret_cast<int8_t*>(take(static_cast<size_t>(N) * static_cast<size_t>(D)));
+    w.e_scale = reinterpret_cast<float*>(take(sizeof(float) * static_cast<size_t>(N)));
   }
   w.bytes = off;
   return w;
 }
 
-// The arguments and tensor maps that every head launch shares.
-cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, const void* C, const void* bias,
-                     const float* c_scale, bool maxima, const HeadWs& w, int sms, cce::HeadArgs* A, CUtensorMap* tmE,
-                     CUtensorMap* tmC) {
-  A->split = make_split(N, V, maxima, std::min(sms, kMaxSms));
+// The arguments and tensor maps that every head launch shares; E and e_scale: the operand's own rows.
+cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, const float* e_scale, const void* C,
+                     const void* bias, const float* c_scale, const HeadWs& w, int sms, cce::HeadArgs* A,
+                     CUtensorMap* tmE, CUtensorMap* tmC) {
+  A->split = make_split(N, V, std::min(sms, kMaxSms));
   A->N = static_cast<int>(N);
   A->D = static_cast<int>(D);
   A->V = static_cast<int>(V);
   const int per_block = int8 ? 128 : 64;  // values of a 128-byte K-block
   A->num_kb = static_cast<int>(ceil_div(D, per_block));
   A->kb_chunk = int8 ? A->num_kb : kChunkBlocks;
-  A->box_c = A->split.unit == cce::kHeadBN ? cce::kHeadBN : 32;
+  A->box_c = A->split.unit;
   A->e_rows = static_cast<int>(std::min<int64_t>(cce::kHeadBM, (N + 7) / 8 * 8));
   A->bias = static_cast<const __nv_bfloat16*>(bias);
-  A->e_scale = w.e_scale;
+  A->e_scale = e_scale;
   A->c_scale = c_scale;
   A->err = &w.hdr->err;
+  A->failed = &w.hdr->failed;
   A->timeout_ns = cce::wait_timeout_ns();
   // Failure-detection test hook: CCE_TEST_INJECT_STALL=4 makes the first bounded wait of the head kernel run out
   // (reported as CCE_ERR_DEVICE_TIMEOUT by cce_check_device_error).
@@ -147,8 +185,7 @@ cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, 
   A->inject_stall = (stall != nullptr && stall[0] == '4') ? 1 : 0;
   const auto type = int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const size_t size = int8 ? 1 : 2;
-  const void* e = int8 ? static_cast<const void*>(w.e8) : E;
-  CCE_CHECK(cce::make_map(tmE, type, size, e, N, D, per_block, static_cast<uint32_t>(A->e_rows)));
+  CCE_CHECK(cce::make_map(tmE, type, size, E, N, D, per_block, static_cast<uint32_t>(A->e_rows)));
   CCE_CHECK(cce::make_map(tmC, type, size, C, V, D, per_block, static_cast<uint32_t>(A->box_c)));
   return CCE_OK;
 }
@@ -197,56 +234,97 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
   CCE_CHECK(cce::check_device(&sms));
   CCE_CHECK(cce::get_encoder());
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(cce::WsHeader), s));
+  const int K = p->num_tokens, top_k = p->top_k;
+  // one memset clears the header and, directly behind it, the first slab's counters
+  CCE_TRY(cudaMemsetAsync(w.hdr, 0, top_k > 0 ? cce::kHeaderBytes + w.counter_bytes : sizeof(cce::WsHeader), s));
   if (!has_rows) return CCE_OK;
-
   if (int8)
     CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), p->N, p->D, w.e8, w.e_scale, s));
-  cce::HeadArgs A{};
-  CUtensorMap tmE, tmC;
-  CCE_CHECK(head_args(p->N, p->D, p->V, int8, E, C, bias, c_scale, tile_max != nullptr, w, sms, &A, &tmE, &tmC));
-  A.tokens = tokens;
-  A.ignore_index = p->ignore_index;
-  A.K = p->num_tokens;
-  A.zt = w.zt;
-  A.tile_max = tile_max;
-  A.inv_t = 1.f / p->temperature;
-  A.part_m = w.part_m;
-  A.part_s = w.part_s;
-  A.part_w = w.part_w;
-  A.lists = w.lists;
-  CCE_TRY(cce::launch_head(tmE, tmC, A, int8, list_len(p->top_k), int8, s));
 
-  cce::HeadFinish F{};
-  F.split = A.split;
-  F.N = A.N;
-  F.D = A.D;
-  F.V = A.V;
-  F.E = static_cast<const __nv_bfloat16*>(E);
-  F.C = int8 ? nullptr : static_cast<const __nv_bfloat16*>(C);
-  F.E8 = w.e8;
-  F.C8 = int8 ? static_cast<const int8_t*>(C) : nullptr;
-  F.e_scale = w.e_scale;
-  F.c_scale = c_scale;
-  F.bias = A.bias;
-  F.tokens = tokens;
-  F.ignore_index = p->ignore_index;
-  F.K = A.K;
-  F.zt = w.zt;
-  F.inv_t = A.inv_t;
-  F.part_m = w.part_m;
-  F.part_s = w.part_s;
-  F.part_w = w.part_w;
-  F.lists = w.lists;
-  F.L = list_len(p->top_k);
-  F.top_k = p->top_k;
-  F.logprobs = logprobs;
-  F.entropy = entropy;
-  F.lse = lse;
-  F.top_logprobs = top_logprobs;
-  F.top_ids = top_ids;
-  F.err = A.err;
-  CCE_TRY(cce::launch_head_finish(F, true, s));
+  const int64_t slab = slab_rows(p->N, top_k);
+  for (int64_t r0 = 0; r0 < p->N; r0 += slab) {
+    const int64_t n = std::min(slab, p->N - r0);
+    const auto* Eb = static_cast<const __nv_bfloat16*>(E) + r0 * p->D;
+    const void* operand = int8 ? static_cast<const void*>(w.e8 + r0 * p->D) : Eb;
+    const float* e_scale = int8 ? w.e_scale + r0 : nullptr;
+    const int64_t* tok = K > 0 ? tokens + r0 * K : nullptr;
+    if (r0 > 0) CCE_TRY(cudaMemsetAsync(w.counters, 0, w.counter_bytes, s));
+    if (K > 1) CCE_TRY(cce::launch_head_tokens(tok, static_cast<int>(n), K, static_cast<int>(p->V), p->ignore_index,
+                                               w.tok_t, s));
+    cce::HeadArgs A{};
+    CUtensorMap tmE, tmC;
+    CCE_CHECK(head_args(n, p->D, p->V, int8, operand, e_scale, C, bias, c_scale, w, sms, &A, &tmE, &tmC));
+    A.tokens = tok;
+    A.tok_t = w.tok_t;
+    A.ignore_index = p->ignore_index;
+    A.K = K;
+    A.zt = w.zt;
+    A.tile_max = tile_max;
+    A.pick_max = top_k > 0 ? w.pick_max : nullptr;
+    A.picks = top_k > 0 ? picks_pitch(p->V) : 0;
+    A.inv_t = 1.f / p->temperature;
+    A.part_m = w.part_m;
+    A.part_s = w.part_s;
+    A.part_w = w.part_w;
+    // it follows a kernel directly where the operands or the tokens were prepared on the stream
+    CCE_TRY(cce::launch_head(tmE, tmC, A, int8, K > 1 || (int8 && r0 == 0), s));
+
+    cce::HeadPicks P{};
+    if (top_k > 0) {
+      P.N = A.N;
+      P.D = A.D;
+      P.V = A.V;
+      P.E = operand;
+      P.C = C;
+      P.e_scale = e_scale;
+      P.c_scale = c_scale;
+      P.bias = A.bias;
+      P.pick_max = w.pick_max;
+      P.picks = A.picks;
+      P.wanted = picks_wanted(top_k);
+      P.done = w.counters;
+      P.count = w.counters + 4;
+      P.base = w.base;
+      P.pick = w.pick;
+      P.slot = w.slot;
+      P.rows = w.rows;
+      P.items = w.items;
+      P.logits = w.logits;
+      CCE_TRY(cce::launch_head_picks(P, int8, sms, s));
+    }
+    cce::HeadFinish F{};
+    F.split = A.split;
+    F.N = A.N;
+    F.D = A.D;
+    F.V = A.V;
+    F.E = Eb;
+    F.C = int8 ? nullptr : static_cast<const __nv_bfloat16*>(C);
+    F.E8 = int8 ? w.e8 + r0 * p->D : nullptr;
+    F.C8 = int8 ? static_cast<const int8_t*>(C) : nullptr;
+    F.e_scale = e_scale;
+    F.c_scale = c_scale;
+    F.bias = A.bias;
+    F.tokens = tok;
+    F.ignore_index = p->ignore_index;
+    F.K = K;
+    F.zt = w.zt;
+    F.inv_t = A.inv_t;
+    F.part_m = w.part_m;
+    F.part_s = w.part_s;
+    F.part_w = w.part_w;
+    F.pick = w.pick;
+    F.logits = w.logits;
+    F.wanted = P.wanted;
+    F.top_k = top_k;
+    F.logprobs = K > 0 ? logprobs + r0 * K : nullptr;
+    F.entropy = K > 0 ? entropy + r0 : nullptr;
+    F.lse = K > 0 ? lse + r0 : nullptr;
+    F.top_logprobs = top_k > 0 ? top_logprobs + r0 * top_k : nullptr;
+    F.top_ids = top_k > 0 ? top_ids + r0 * top_k : nullptr;
+    F.err = A.err;
+    F.failed = A.failed;
+    CCE_TRY(cce::launch_head_finish(F, s));
+  }
   return CCE_OK;
 }
 
@@ -333,11 +411,11 @@ cce_status cce_int8_linear(int64_t N, int64_t D, int64_t V, const void* E, const
   CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), N, D, w.e8, w.e_scale, s));
   cce::HeadArgs A{};
   CUtensorMap tmE, tmC;
-  CCE_CHECK(head_args(N, D, V, true, E, C, bias, c_scale, false, w, sms, &A, &tmE, &tmC));
+  CCE_CHECK(head_args(N, D, V, true, w.e8, w.e_scale, C, bias, c_scale, w, sms, &A, &tmE, &tmC));
   A.inv_t = 1.f;
   A.out = out;
   A.out_fp32 = out_fp32;
-  CCE_TRY(cce::launch_head(tmE, tmC, A, true, 0, true, s));
+  CCE_TRY(cce::launch_head(tmE, tmC, A, true, true, s));
   return CCE_OK;
 }
 

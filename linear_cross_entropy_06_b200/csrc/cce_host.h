@@ -19,6 +19,7 @@ struct WsHeader {
   int err;   // device error word
   int done;  // blocks of the forward's finish kernel that are done
   int bar;   // grid barrier counter of the backward's planning launch
+  int failed;  // set by the head kernel when a bounded wait ran out
 };
 
 // Sets the message of cce_last_error_message() and returns s.
