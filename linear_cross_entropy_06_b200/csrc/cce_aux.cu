@@ -285,47 +285,6 @@ int grid_for(int64_t items, int per_block, int cap) {
   return static_cast<int>(g < cap ? (g > 0 ? g : 1) : cap);
 }
 
-// One block per row, see LogprobPrep: warp 0 forms the row's coefficients, then every thread copies E.
-constexpr int kPrepThreads = 128;
-
-__global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid_constant__ LogprobPrep P) {
-  __shared__ int keep;
-  const int r = blockIdx.x, lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    const float lse = P.lse_in[r];
-    const bool fine = lse != -INFINITY;  // a NaN goes on as NaN
-    float sum = 0.f;
-    bool any = false;
-    for (int k0 = 0; k0 < P.K; k0 += 32) {
-      const int k = k0 + lane;
-      if (k < P.K) {
-        const int64_t id = P.tokens[static_cast<int64_t>(r) * P.K + k];
-        const bool here = id != P.ignore_index && id >= 0 && id < P.V;
-        const float g = here && fine && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + k] : 0.f;
-        any = any || here;
-        sum += g;
-        P.tok[static_cast<int64_t>(k) * P.N + r] = here && fine ? static_cast<int>(id) : -1;
-        P.tok_g[static_cast<int64_t>(k) * P.N + r] = g * P.inv_t;
-      }
-    }
-    any = __any_sync(0xffffffffu, any) && fine;
-    sum = warp_sum(sum);
-    if (lane == 0) {
-      const float h = any && P.g_entropy != nullptr ? P.g_entropy[r] : 0.f;
-      P.coef[r] = any ? -P.inv_t * (h != 0.f ? fmaf(h, P.entropy[r], sum) : sum) : 0.f;
-      P.coef_log[r] = any ? -P.inv_t * h : 0.f;
-      P.lse[r] = any ? lse : INFINITY;
-      P.targets[r] = any ? P.V : P.masked_id;
-      if (r == 0) *P.one = 1.f;
-      keep = any;
-    }
-  }
-  __syncthreads();
-  const uint4* src = reinterpret_cast<const uint4*>(P.E + static_cast<int64_t>(r) * P.D);
-  uint4* dst = reinterpret_cast<uint4*>(P.E_out + static_cast<int64_t>(r) * P.D);
-  for (int d = threadIdx.x; d < P.D / 8; d += kPrepThreads) dst[d] = keep ? src[d] : make_uint4(0, 0, 0, 0);
-}
-
 }  // namespace
 
 cudaError_t launch_fwd_finish(const FwdFinish& F, bool after_kernel, cudaStream_t s) {
@@ -364,12 +323,6 @@ cudaError_t launch_weighted_colsum(const __nv_bfloat16* X, int64_t rows, int64_t
   if (e != cudaSuccess || rows == 0) return e;
   weighted_colsum_kernel<<<static_cast<int>((rows + kColsumRows - 1) / kColsumRows), 256, 0, s>>>(X, rows, D, w,
                                                                                                  extra, out);
-  note_launches(1);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_logprob_prep(const LogprobPrep& P, cudaStream_t s) {
-  logprob_prep_kernel<<<P.N, kPrepThreads, 0, s>>>(P);
   note_launches(1);
   return cudaGetLastError();
 }

@@ -16,7 +16,8 @@
 //          of the fp32 G are added into it.
 //   dE     (row block b, 256-column slice s of D): sum over the kept halves h of the chunk's listed
 //          tiles t of G_bth C_th[:, s] in TMEM, then one fp32 TMA reduce-add into dE_acc
-//          (split-reduce over chunks).
+//          (split-reduce over chunks; for log-probabilities with few row blocks and slices also over de_split
+//          shares of the chunk's tiles, since these items are the longest).
 //   dC     (vocabulary tile t, slice s): sum over the listed b of G_bt^T E_b[:, s] in TMEM (A = the
 //          same G tile read MN-major, a skipped half read as zeros), plus the onehot terms of rows
 //          whose target half in t was skipped and the label-smoothing term, written once by TMA
@@ -187,7 +188,7 @@ __device__ __forceinline__ void decode_item(int w, int g, int g_begin, int nchun
     if (c >= kGradBuffers) {  // the buffer's previous chunk must have been read by its dE / dC items
       const int prev = c - kGradBuffers;
       it.dep_idx = A.ctr_b_done + prev;
-      it.dep_val = (A.nde[prev] + A.ndc[prev]) * A.S;
+      it.dep_val = (A.nde[prev] * A.de_split + A.ndc[prev]) * A.S;
     } else {
       it.dep_idx = -1;
       it.dep_val = 0;
@@ -199,19 +200,22 @@ __device__ __forceinline__ void decode_item(int w, int g, int g_begin, int nchun
     const int nde = A.nde[c];
     it.slot0 = A.offsets_t[t_begin];
     it.slot1 = 0;
-    if (local < nde * S) {  // slice-major: concurrent dE items read the same columns of C
+    const int n_de = nde * S * A.de_split;
+    if (local < n_de) {  // slice-major: concurrent dE items read the same columns of C
+      const int l = local / A.de_split, part = local - l * A.de_split;
       it.kind = kDE;
-      it.key = A.de_list[static_cast<int64_t>(c) * A.nb + local % nde];
+      it.key = A.de_list[static_cast<int64_t>(c) * A.nb + l % nde];
       // serpentine over chunks: a chunk starts on the slices of dE the previous one touched last
-      it.s = (c & 1) ? S - 1 - local / nde : local / nde;
+      it.s = (c & 1) ? S - 1 - l / nde : l / nde;
       const int2 r = A.rb_range[static_cast<int64_t>(c) * A.nb + it.key];
-      it.begin = r.x;
-      it.end = r.y;
-      it.slot1 = A.hp_b[r.y] - A.hp_b[r.x];
+      const int len = (r.y - r.x + A.de_split - 1) / A.de_split;
+      it.begin = min(r.y, r.x + part * len);
+      it.end = min(r.y, it.begin + len);
+      it.slot1 = A.hp_b[it.end] - A.hp_b[it.begin];
       it.dep_idx = A.ctr_g_b + c * A.nb + it.key;
-      it.dep_val = it.slot1;  // every kept half of the row block in the chunk is stored
+      it.dep_val = A.hp_b[r.y] - A.hp_b[r.x];  // every kept half of the row block in the chunk is stored
     } else {  // slice-major too: concurrent dC items read the same columns of E
-      const int v = local - nde * S;
+      const int v = local - n_de;
       const int ndc = A.ndc[c];
       it.kind = kDC;
       it.key = A.vt_order[t_begin + v % ndc];

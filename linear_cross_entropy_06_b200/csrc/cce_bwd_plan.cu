@@ -174,6 +174,14 @@ __device__ void tile_flags_unit(const PlanArgs& A, int group, int b, int t0) {
   if (tid < kFlagTiles) any_target[group][tid] = 0;
   if (tid == 0) forced[group] = 0;
   const int64_t j0 = 2 * static_cast<int64_t>(t0);  // the run's first half (saved sub-tile)
+  unsigned mine = 0;  // the run's halves that hold a token of the row
+  if (A.tok != nullptr && A.filter_on && row_in) {
+    for (int k = 0; k < A.K; ++k) {
+      const int id = A.tok[static_cast<int64_t>(k) * A.N + r];
+      const int64_t h = id / kSubTile - j0;
+      if (id >= 0 && h >= 0 && h < 2 * kFlagTiles) mine |= 1u << h;
+    }
+  }
   float mt[2 * kFlagTiles];
 #pragma unroll
   for (int k = 0; k < 2 * kFlagTiles; ++k)
@@ -185,12 +193,7 @@ __device__ void tile_flags_unit(const PlanArgs& A, int group, int b, int t0) {
   const bool local = valid && valid_target(tr - A.vs, A.V, A.ignore_index - A.vs);  // its target is in this shard
   tr -= A.vs;
   if (local && tr / kBwdBN >= t0 && tr / kBwdBN < t0 + kFlagTiles) any_target[group][tr / kBwdBN - t0] = 1;
-  if (A.tok != nullptr && A.filter_on && row_in) {
-    for (int k = 0; k < A.K; ++k) {
-      const int64_t h = A.tok[static_cast<int64_t>(k) * A.N + r] / kSubTile - j0;
-      if (A.tok[static_cast<int64_t>(k) * A.N + r] >= 0 && h >= 0 && h < 2 * kFlagTiles) atomicOr(&forced[group], 1u << h);
-    }
-  }
+  if (mine != 0) atomicOr(&forced[group], mine);
 #pragma unroll
   for (int k = 0; k < 2 * kFlagTiles; ++k) mt[k] = valid ? mt[k] - l : -INFINITY;
   wmax[group][tid >> 5][lane] = warp_column_max32(mt, lane);  // lane k: the warp's max of half j0 + k
@@ -655,6 +658,126 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   if (threadIdx.x == 0) *A.filtered_tiles = static_cast<int64_t>(nb) * A.T - static_cast<int64_t>(*P.kept_total);
 }
 
+// The plan when nothing is skipped, in closed form and without a grid barrier: every tile is listed with every half of
+// it, chunks have chunk_vt vocabulary tiles each, and a row block's quads in a chunk are its halves four by four. The
+// planning launch's nine phases cost 47 us at 256 x 128 x 4096 and 69 us at 4096 x 4096 x 128256, this 3 and 9 us
+// more than the rows' own work. gtid / gthreads: the calling thread among those that share the plan.
+__device__ void dense_plan(const PlanArgs& A, int64_t gtid, int64_t gthreads) {
+  const BwdPlan& P = A.P;
+  const int nb = P.nb, nt = P.nt, n = P.nchunks, T = static_cast<int>(A.T);
+  const int full = (2 * P.chunk_vt + 3) / 4;  // quads of a row block in a whole chunk
+  const int64_t tiles = static_cast<int64_t>(nb) * nt;
+  auto tile_halves = [&](int t) { return 2 * t + 1 < T ? 3 : 1; };
+  auto chunk_halves = [&](int c) { return min(T, 2 * min(nt, (c + 1) * P.chunk_vt)) - 2 * c * P.chunk_vt; };
+  for (int64_t i = gtid; i < tiles; i += gthreads) {
+    const int t = static_cast<int>(i / nb), b = static_cast<int>(i % nb);  // slot i: by vocabulary tile
+    const int f = kFlagListed | (tile_halves(t) << 2);
+    const int64_t o = static_cast<int64_t>(b) * nt + t;
+    P.flags[o] = static_cast<uint8_t>(f);
+    P.entries_t[i] = make_int2(b * 16 + f, t);
+    P.entries_b[o] = make_int2(t, static_cast<int>(i) | (tile_halves(t) << kSlotBits));
+    P.hp_b[o] = b * T + 2 * t;
+  }
+  for (int64_t t = gtid; t <= nt; t += gthreads) {
+    P.offsets_t[t] = static_cast<int>(t) * nb;
+    P.oh_off[t] = 0;
+    if (t == nt) break;
+    const int c = static_cast<int>(t) / P.chunk_vt, in = static_cast<int>(t) - c * P.chunk_vt;
+    P.pstart_t[t] = (c * full + (in + 1) / 2) * nb;
+    P.cnt_ht[t] = nb * (tile_halves(static_cast<int>(t)) == 3 ? 2 : 1);
+    P.vt_order[t] = static_cast<int>(t);
+  }
+  for (int64_t i = gtid; i < static_cast<int64_t>(n) * nb; i += gthreads) {
+    const int c = static_cast<int>(i / nb), b = static_cast<int>(i % nb);
+    P.rb_range[i] = make_int2(b * nt + c * P.chunk_vt, b * nt + min(nt, (c + 1) * P.chunk_vt));
+    P.de_list[i] = b;
+  }
+  for (int64_t i = gtid; i < static_cast<int64_t>(n) * full * nb; i += gthreads) {
+    const int c = static_cast<int>(i / (static_cast<int64_t>(full) * nb));
+    const int j = static_cast<int>(i / nb) - c * full, b = static_cast<int>(i % nb);
+    const int left = chunk_halves(c) - 4 * j, h = 2 * c * P.chunk_vt + 4 * j;
+    if (left <= 0) continue;
+    const int s0 = 2 * j * nb + b, s1 = s0 + nb;  // slots of the quad's two tiles, relative to the chunk
+    P.quad_b[i] = b;
+    P.quad_h[i] = make_int4(h, left > 1 ? h + 1 : -1, left > 2 ? h + 2 : -1, left > 3 ? h + 3 : -1);
+    P.quad_s[i] = make_int4(s0, s0, s1, s1);
+  }
+  for (int64_t c = gtid; c <= n; c += gthreads) {
+    P.chunk_t[c] = static_cast<int>(min(static_cast<int64_t>(nt), c * P.chunk_vt));
+    if (c == n) break;
+    P.ndc[c] = min(nt, static_cast<int>(c + 1) * P.chunk_vt) - static_cast<int>(c) * P.chunk_vt;
+    P.nde[c] = nb;
+  }
+  if (gtid == 0) {  // the queue: quads(0), then quads(c) and dE/dC(c - 1), then dE/dC(n - 1)
+    auto quads = [&](int c) { return (chunk_halves(c) + 3) / 4 * nb; };
+    auto sums = [&](int c) { return (nb * A.de_split + min(nt, (c + 1) * P.chunk_vt) - c * P.chunk_vt) * P.S; };
+    int at = 0, g = 0;
+    P.grp_start[g] = 0;
+    P.grp_start[++g] = at += quads(0);
+    for (int c = 1; c < n; ++c) {
+      P.grp_start[++g] = at += quads(c);
+      P.grp_start[++g] = at += sums(c - 1);
+    }
+    P.grp_start[++g] = at += sums(n - 1);
+    P.hp_b[tiles] = nb * T;
+    *P.nchunks_dev = n;
+    *P.n_empty = 0;
+    *A.filtered_tiles = 0;
+  }
+  for (int64_t i = gtid; i < A.sync_ints; i += gthreads) A.sync[i] = 0;
+  for (int64_t i = gtid; i < kZeroHalfBytes / 16; i += gthreads)
+    reinterpret_cast<float4*>(A.zero_half)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (A.dbias_acc != nullptr)
+    for (int64_t i = gtid; i < A.V; i += gthreads) A.dbias_acc[i] = 0.f;
+}
+
+// Block r < N: row r, see LogprobPrep (warp 0 forms the row's coefficients, then every thread copies E). The blocks
+// behind them, when nothing is skipped, share the plan; the rows' blocks then also zero dE_acc.
+constexpr int kPrepThreads = 128;
+
+__global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid_constant__ LogprobPrep P,
+                                                                    const __grid_constant__ PlanArgs A) {
+  __shared__ int keep;
+  const int r = blockIdx.x, lane = threadIdx.x & 31;
+  if (r >= P.N) {
+    dense_plan(A, static_cast<int64_t>(r - P.N) * kPrepThreads + threadIdx.x,
+               static_cast<int64_t>(gridDim.x - P.N) * kPrepThreads);
+    return;
+  }
+  if (threadIdx.x < 32) {
+    const float lse = P.lse_in[r];
+    const bool fine = lse != -INFINITY;  // a NaN goes on as NaN
+    float sum = 0.f;
+    bool any = false;
+    if (lane < P.K) {
+      const int64_t id = P.tokens[static_cast<int64_t>(r) * P.K + lane];
+      any = id != P.ignore_index && id >= 0 && id < P.V;
+      sum = any && fine && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + lane] : 0.f;
+      P.tok[static_cast<int64_t>(lane) * P.N + r] = any && fine ? static_cast<int>(id) : -1;
+      P.tok_g[static_cast<int64_t>(lane) * P.N + r] = sum * P.inv_t;
+    }
+    any = __any_sync(0xffffffffu, any) && fine;
+    sum = warp_sum(sum);
+    if (lane == 0) {
+      const float h = any && P.g_entropy != nullptr ? P.g_entropy[r] : 0.f;
+      P.coef[r] = any ? -P.inv_t * (h != 0.f ? fmaf(h, P.entropy[r], sum) : sum) : 0.f;
+      P.coef_log[r] = any ? -P.inv_t * h : 0.f;
+      P.lse[r] = any ? lse : INFINITY;
+      P.targets[r] = any ? P.V : P.masked_id;
+      A.scale[r] = 1.f;
+      if (r == 0) *P.one = 1.f;
+      keep = any;
+    }
+  }
+  __syncthreads();
+  const uint4* src = reinterpret_cast<const uint4*>(P.E + static_cast<int64_t>(r) * P.D);
+  uint4* dst = reinterpret_cast<uint4*>(P.E_out + static_cast<int64_t>(r) * P.D);
+  for (int d = threadIdx.x; d < P.D / 8; d += kPrepThreads) dst[d] = keep ? src[d] : make_uint4(0, 0, 0, 0);
+  if (A.filter_on) return;
+  float4* acc = reinterpret_cast<float4*>(A.dE_acc + static_cast<int64_t>(r) * P.D);
+  for (int d = threadIdx.x; d < P.D / 4; d += kPrepThreads) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
 // The element-wise steps of the backward after the tensor-core kernel, in two launches:
 //  empty_tiles_kernel: dC rows of the vocabulary tiles no row block lists. Every logit of such a
 //   tile is skipped, so only the target part of the logit gradient reaches them (Loss functions
@@ -859,6 +982,13 @@ __global__ void skip_map_kernel(const uint8_t* __restrict__ flags, int nt, int64
 
 }  // namespace
 
+cudaError_t launch_logprob_prep(const LogprobPrep& P, const PlanArgs& A, int num_sms, cudaStream_t s) {
+  const int plan_blocks = A.filter_on ? 0 : num_sms;
+  logprob_prep_kernel<<<P.N + plan_blocks, kPrepThreads, 0, s>>>(P, A);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_empty_tiles(const BwdFinalize& F, int num_sms, bool after_kernel, cudaStream_t s) {
   if (F.N == 0) return cudaSuccess;
   const int64_t es = F.dc_bf16 ? 2 : 4, rowbytes = F.D * es;
@@ -880,10 +1010,14 @@ cudaError_t launch_empty_tiles(const BwdFinalize& F, int num_sms, bool after_ker
   return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_finalize(const BwdFinalize& F, int num_sms, cudaStream_t s) {
+cudaError_t launch_bwd_finalize(const BwdFinalize& F, int num_sms, bool after_kernel, cudaStream_t s) {
   if (F.N == 0) return cudaSuccess;
-  const cudaError_t e = launch_after_previous(bwd_finalize_kernel, dim3(num_sms * 4), dim3(256), 0, s, F);
-  if (e != cudaSuccess) return e;
+  if (after_kernel) {
+    const cudaError_t e = launch_after_previous(bwd_finalize_kernel, dim3(num_sms * 4), dim3(256), 0, s, F);
+    if (e != cudaSuccess) return e;
+  } else {
+    bwd_finalize_kernel<<<num_sms * 4, 256, 0, s>>>(F);
+  }
   note_launches(1);
   return cudaGetLastError();
 }

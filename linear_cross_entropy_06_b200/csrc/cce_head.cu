@@ -134,6 +134,12 @@ struct HeadTile {
   bool first, last;  // of the segment
 };
 
+// Rows of C that a tile loads and multiplies: all 256 in one box, or those it needs 64 at a time (one box a stage
+// instead of four: 896 x 2048 x 50257: 161 us against 182).
+__device__ __forceinline__ int tile_rows(const HeadTile& t) {
+  return (t.ncol + kHeadUnit - 1) / kHeadUnit * kHeadUnit;
+}
+
 // Calls f(tile) for every tile of this block, in the order that all roles share; f returns false to stop. Within a
 // segment the walk starts at the tile whose position is 0 modulo the length of a block's share: the blocks on
 // different row blocks then pass the same columns of C at about the same time, and C is read from HBM about once
@@ -291,7 +297,7 @@ __device__ __forceinline__ void write_logits(const HeadArgs& A, const float (&a)
 template <bool I8, bool OUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     head_kernel(const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmC,
-                const __grid_constant__ HeadArgs A) {
+                const __grid_constant__ CUtensorMap tmC64, const __grid_constant__ HeadArgs A) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* scratch = base + STAGES * STAGE_BYTES;
@@ -491,17 +497,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t issued[STAGES] = {0, 0, 0, 0};
       bool ok = true;
       const uint32_t e_bytes = static_cast<uint32_t>(A.e_rows) * KB_BYTES;
-      const uint32_t box_bytes = static_cast<uint32_t>(A.box_c) * KB_BYTES;
       for_tiles(A.split, A.V, [&](const HeadTile& t) {
-        const int nbox = (t.ncol + A.box_c - 1) / A.box_c;
+        const int rows_c = tile_rows(t);
+        const uint32_t bytes = e_bytes + static_cast<uint32_t>(rows_c) * KB_BYTES;
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) return ok = false;
           const uint32_t dst = smem_u32(base + stage * STAGE_BYTES);
-          mbar_arrive_expect_tx(full_bar(stage), e_bytes + static_cast<uint32_t>(nbox) * box_bytes);
+          mbar_arrive_expect_tx(full_bar(stage), bytes);
           tma_load_2d(dst, &tmE, full_bar(stage), kb * KE, t.b * BM);
-          for (int j = 0; j < nbox; ++j)
-            tma_load_2d(dst + A_BYTES + static_cast<uint32_t>(j) * box_bytes, &tmC, full_bar(stage), kb * KE,
-                        t.col + j * A.box_c);
+          if (rows_c == BN) {
+            tma_load_2d(dst + A_BYTES, &tmC, full_bar(stage), kb * KE, t.col);
+          } else {
+            for (int j = 0; j < rows_c; j += kHeadUnit)
+              tma_load_2d(dst + A_BYTES + static_cast<uint32_t>(j) * KB_BYTES, &tmC64, full_bar(stage), kb * KE,
+                          t.col + j);
+          }
           ++issued[stage];
           if (++stage == STAGES) {
             stage = 0;
@@ -522,7 +532,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, issued_any = false;
       for_tiles(A.split, A.V, [&](const HeadTile& t) {
-        const uint32_t idesc = idesc_n(I8, (t.ncol + A.box_c - 1) / A.box_c * A.box_c);
+        const uint32_t idesc = idesc_n(I8, tile_rows(t));
         for (int k0 = 0; k0 < num_kb; k0 += A.kb_chunk) {
           if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, wc)) return ok = false;
           tc_fence_after();
@@ -709,91 +719,139 @@ __device__ __forceinline__ unsigned long long warp_sort(unsigned long long key, 
   return key;
 }
 
-constexpr int kPickWarpsMax = 32;
-constexpr int kPickHeld = 16;  // maxima a lane holds at a time
+constexpr int kPickGroups = 256; // groups of maxima of a row in the sieve
+constexpr int kPickHeld = 16;    // maxima a lane holds at a time
+constexpr int kPickSifted = 512; // candidates kept by the sieve
 
-// One block per row. Every warp takes its share of the maxima, 512 at a time: the best W of those and of what it
-// kept before. The best W of what the warps kept are the row's picks.
-// The last block to finish lays out the picks' rows: every pick that some row wants gets its place in `rows` and
-// one work item for each 64 of its rows (in any order: nothing depends on it); with few rows it also does the
-// work of head_scatter_kernel.
-__global__ void __launch_bounds__(kPickWarpsMax * 32) head_pick_kernel(const __grid_constant__ HeadPicks P) {
-  __shared__ unsigned long long kept[kPickWarpsMax][32];
+// The W best of `count` keys in shared memory, to out[0 ..] (which may be the same memory), by one warp that holds
+// R in each lane; returns how many.
+template <int R>
+__device__ __forceinline__ int warp_best(const unsigned long long* keys, int count, int W, int lane,
+                                         unsigned long long* out) {
+  unsigned long long key[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) key[i] = 32 * i + lane < count ? keys[32 * i + lane] : 0ull;
+  __syncwarp();
+  const int m = warp_collect(key, warp_bound(key, W), lane, out);
+  __syncwarp();
+  return min(m, W);
+}
+
+// One block per row. A sieve first: the maxima are dealt to 256 groups, and the W-th largest of the groups' largest is
+// a bound that at least W maxima reach, and few more, as the best W sit in almost as many groups. What reaches it is
+// collected (about W + 2), and the best W of that are the row's picks.
+// Where more than kPickSifted reach the bound (equal logits), every warp bisects over its share, 512 maxima at a
+// time together with what it kept before, and the best W of what the warps kept are the picks.
+// P.grouped: the last block to finish lays out the picks' rows: every pick that some row wants gets its place in
+// `rows` and one work item for each 64 of its rows (in any order: nothing depends on it).
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 5 : 1)
+    head_pick_kernel(const __grid_constant__ HeadPicks P) {
+  constexpr int kKeys = WARPS * 32 > kPickSifted ? WARPS * 32 : kPickSifted;
+  static_assert(kPickGroups <= kKeys && WARPS * 32 % kPickGroups == 0, "groups share the keys' memory");
+  __shared__ unsigned long long keys[kKeys];
+  __shared__ unsigned long long bound_s;
+  __shared__ int sifted;
   __shared__ int last;
   __shared__ int placed[2];  // rows and work items so far
   if (threadIdx.x < 2) placed[threadIdx.x] = 0;
+  if (threadIdx.x == 0) sifted = 0;
   wait_for_previous_grid();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int r = blockIdx.x, W = P.wanted;
   const int n = (P.V + kHeadPick - 1) / kHeadPick;
   const float* mx = P.pick_max + static_cast<int64_t>(r) * P.picks;
-  const int share = (n + nw * 32 - 1) / (nw * 32) * 32;
-  const int u1 = min(n, (w + 1) * share);
-  unsigned long long mine = 0;  // lane i: a key that the warp has kept
-  for (int u0 = w * share; u0 < u1; u0 += 32 * kPickHeld) {
-    unsigned long long key[kPickHeld + 1];
-    float v[kPickHeld];
-#pragma unroll
-    for (int j = 0; j < kPickHeld; ++j) v[j] = u0 + 32 * j + lane < u1 ? mx[u0 + 32 * j + lane] : 0.f;
-#pragma unroll
-    for (int j = 0; j < kPickHeld; ++j) {
-      const int u = u0 + 32 * j + lane;
-      key[j] = u < u1 ? make_key(v[j], static_cast<uint32_t>(u)) : 0ull;
-    }
-    key[kPickHeld] = mine;
-    const unsigned long long bound = warp_bound(key, W);
-    const int m = warp_collect(key, bound, lane, kept[w]);
-    __syncwarp();
-    mine = lane < min(m, W) ? kept[w][lane] : 0ull;
-    __syncwarp();
+  unsigned long long best = 0;
+#pragma unroll 8
+  for (int u = threadIdx.x; u < n; u += WARPS * 32) {
+    const unsigned long long x = make_key(mx[u], static_cast<uint32_t>(u));
+    best = x > best ? x : best;
   }
-  kept[w][lane] = mine;
+  constexpr int lanes = WARPS * 32 / kPickGroups;  // of a group: neighbours
+#pragma unroll
+  for (int o = 1; o < lanes; o <<= 1) {
+    const unsigned long long x = __shfl_xor_sync(0xffffffffu, best, o);
+    best = x > best ? x : best;
+  }
+  if (threadIdx.x % lanes == 0) keys[threadIdx.x / lanes] = best;
   __syncthreads();
   if (w == 0) {
-    unsigned long long key[kPickWarpsMax];
+    unsigned long long key[kPickGroups / 32];
 #pragma unroll
-    for (int i = 0; i < kPickWarpsMax; ++i) key[i] = i < nw ? kept[i][lane] : 0ull;
-    const unsigned long long bound = warp_bound(key, W);
-    __syncwarp();
-    const int m = min(W, warp_collect(key, bound, lane, kept[0]));
-    __syncwarp();
-    int unit = -1, slot = 0;
-    if (lane < m) {
-      unit = key_column(kept[0][lane]);
-      slot = atomicAdd(P.count + unit, 1);
-    }
-    P.pick[static_cast<int64_t>(r) * 32 + lane] = unit;
-    P.slot[static_cast<int64_t>(r) * 32 + lane] = slot;
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) last = atomicAdd(P.done, 1) == static_cast<int>(gridDim.x) - 1;
+    for (int i = 0; i < kPickGroups / 32; ++i) key[i] = keys[32 * i + lane];
+    int groups = 0;  // that hold anything: with fewer than W of them (a few dozen maxima) all maxima go on
+#pragma unroll
+    for (int i = 0; i < kPickGroups / 32; ++i) groups += key[i] != 0 ? 1 : 0;
+    groups = __reduce_add_sync(0xffffffffu, groups);
+    const unsigned long long bound = groups < W ? 1 : warp_bound(key, W);
+    if (lane == 0) bound_s = bound;
   }
+  __syncthreads();
+  const unsigned long long bound = bound_s;
+#pragma unroll 8
+  for (int u = threadIdx.x; u < n; u += WARPS * 32) {
+    const unsigned long long x = make_key(mx[u], static_cast<uint32_t>(u));
+    if (x >= bound) {
+      const int at = atomicAdd(&sifted, 1);
+      if (at < kPickSifted) keys[at] = x;
+    }
+  }
+  __syncthreads();
+  const bool sieve = sifted <= kPickSifted;
+  if (!sieve) {
+    const int share = (n + WARPS * 32 - 1) / (WARPS * 32) * 32;
+    const int u1 = min(n, (w + 1) * share);
+    unsigned long long* kept = keys + 32 * w;
+    unsigned long long mine = 0;  // lane i: a key that the warp has kept
+    for (int u0 = w * share; u0 < u1; u0 += 32 * kPickHeld) {
+      unsigned long long key[kPickHeld + 1];
+#pragma unroll
+      for (int j = 0; j < kPickHeld; ++j) {
+        const int u = u0 + 32 * j + lane;
+        key[j] = u < u1 ? make_key(mx[u], static_cast<uint32_t>(u)) : 0ull;
+      }
+      key[kPickHeld] = mine;
+      const int m = warp_collect(key, warp_bound(key, W), lane, kept);
+      __syncwarp();
+      mine = lane < min(m, W) ? kept[lane] : 0ull;
+      __syncwarp();
+    }
+    kept[lane] = mine;
+    __syncthreads();
+  }
+  if (w == 0) {
+    const int count = sieve ? sifted : 32 * WARPS;
+    const int m = count <= 64 ? warp_best<2>(keys, count, W, lane, keys) : warp_best<kKeys / 32>(keys, count, W, lane, keys);
+    const int unit = lane < m ? key_column(keys[lane]) : -1;
+    P.pick[static_cast<int64_t>(r) * 32 + lane] = unit;
+    if (P.grouped) {
+      P.slot[static_cast<int64_t>(r) * 32 + lane] = unit >= 0 ? atomicAdd(P.count + unit, 1) : 0;
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) last = atomicAdd(P.done, 1) == static_cast<int>(gridDim.x) - 1;
+    }
+  }
+  if (!P.grouped) return;
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // by picks, or, with few rows, by the pairs (row, pick) that came first to their pick
-  const bool by_pair = P.N * 32 < n;
-  const int limit = by_pair ? P.N * 32 : n;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < limit; i += blockDim.x) {
-    int u = i;
-    if (by_pair) u = __ldcg(P.slot + i) == 0 ? __ldcg(P.pick + i) : -1;
-    const int c = u >= 0 ? __ldcg(P.count + u) : 0;
-    if (c == 0) continue;
-    const int items = (c + kHeadDotRows - 1) / kHeadDotRows;
-    const int at = atomicAdd(&placed[0], c), it = atomicAdd(&placed[1], items);
-    P.base[u] = at;
-    for (int k = 0; k < items; ++k)
-      P.items[it + k] = make_int3(u, at + k * kHeadDotRows, min(kHeadDotRows, c - k * kHeadDotRows));
+  constexpr int kAhead = 8;
+  for (int u0 = threadIdx.x; u0 < n; u0 += WARPS * 32 * kAhead) {
+    int c[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) c[i] = u0 + WARPS * 32 * i < n ? __ldcg(P.count + u0 + WARPS * 32 * i) : 0;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (c[i] == 0) continue;
+      const int u = u0 + WARPS * 32 * i, items = (c[i] + kHeadDotRows - 1) / kHeadDotRows;
+      const int at = atomicAdd(&placed[0], c[i]), it = atomicAdd(&placed[1], items);
+      P.base[u] = at;
+      for (int k = 0; k < items; ++k)
+        P.items[it + k] = make_int3(u, at + k * kHeadDotRows, min(kHeadDotRows, c[i] - k * kHeadDotRows));
+    }
   }
   __syncthreads();
   if (threadIdx.x == 0) P.done[1] = placed[1];
-  if (P.scatter_here) {
-    for (int p = threadIdx.x; p < P.N * 32; p += blockDim.x) {
-      const int u = __ldcg(P.pick + p);
-      if (u >= 0) P.rows[P.base[u] + __ldcg(P.slot + p)] = p;
-    }
-  }
 }
 
 __global__ void __launch_bounds__(256) head_scatter_kernel(const __grid_constant__ HeadPicks P) {
@@ -822,18 +880,19 @@ __device__ __forceinline__ void mma_16x8(int (&c)[4], uint32_t a0, uint32_t a1, 
 }
 
 // A work item: 16 columns x up to 64 gathered rows. The operands are the rows themselves, read 64 bytes a row and
-// step: the eight warps take every eighth step and their sums are added through shared memory. A lane's 16 bytes
+// step: the WARPS warps take the steps in turn and their sums are added through shared memory. Four warps, and four
+// blocks an SM, where there are many items (2048 rows of D = 2048: 116 us, 120 with eight warps and two blocks),
+// eight where there are few and each should be done soon. A lane's 16 bytes
 // of a row feed two instructions whose K positions are the same bytes of both operands, so nothing is rearranged.
 // Rows picked by index suit neither a TMA box nor an M = 128 tile (a pick has 7 rows of 2048 on average); the warp
 // instruction's 16-row tile wastes little, and the kernel is bound by reading C once.
-constexpr int kDotWarps = 8;
 constexpr int kDotStep = 64;  // bytes of a row a step
-// Steps summed in one accumulator: 512 values a warp and part (see the head of the file).
-constexpr int kDotPart = 512 * 2 / kDotStep * kDotWarps;
+// Steps of a warp summed in one accumulator: 512 values (see the head of the file).
+constexpr int kDotPart = 512 * 2 / kDotStep;
 
-template <bool I8, int TILES, int UNROLL, typename Acc>
+template <bool I8, int WARPS, int TILES, int UNROLL, typename Acc>
 __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, const int* ids,
-                                         Acc (*red)[kHeadDotRows * kHeadPick], int64_t pitch, int lane, int w) {
+                                         Acc* red, int64_t pitch, int lane, int w) {
   const int g = lane >> 2, t = lane & 3;
   const int steps = static_cast<int>((pitch + kDotStep - 1) / kDotStep);
   const char* er[TILES][2];
@@ -847,15 +906,15 @@ __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, co
   for (int nt = 0; nt < 2; ++nt)
     cr[nt] = static_cast<const char*>(P.C) + min(pick * kHeadPick + 8 * nt + g, P.V - 1) * pitch + t * 16;
   Acc sum[TILES][2][4] = {};
-  for (int s0 = 0; s0 < steps; s0 += kDotPart) {
+  for (int s0 = 0; s0 < steps; s0 += kDotPart * WARPS) {
     Acc acc[TILES][2][4] = {};
-    const int s1 = min(steps, s0 + kDotPart);
-    for (int s = s0 + w; s < s1; s += kDotWarps * UNROLL) {
+    const int s1 = min(steps, s0 + kDotPart * WARPS);
+    for (int s = s0 + w; s < s1; s += WARPS * UNROLL) {
       uint4 b[UNROLL][2], a[UNROLL][TILES][2];
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
-        const int64_t off = static_cast<int64_t>(s + u * kDotWarps) * kDotStep;
-        const bool in = s + u * kDotWarps < s1 && off + t * 16 < pitch;
+        const int64_t off = static_cast<int64_t>(s + u * WARPS) * kDotStep;
+        const bool in = s + u * WARPS < s1 && off + t * 16 < pitch;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) b[u][nt] = in ? ld_global_nc_v4(cr[nt] + off) : make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -888,30 +947,31 @@ __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, co
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        red[w][(16 * mt + g + 8 * (i >> 1)) * kHeadPick + 8 * nt + 2 * t + (i & 1)] = sum[mt][nt][i];
+        red[(16 * mt + g + 8 * (i >> 1)) * kHeadPick + 8 * nt + 2 * t + (i & 1)] = sum[mt][nt][i];
 }
 
-template <bool I8>
-__global__ void __launch_bounds__(kDotWarps * 32, 2) head_dots_kernel(const __grid_constant__ HeadPicks P) {
+template <bool I8, int WARPS, int ROWS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) head_dots_kernel(const __grid_constant__ HeadPicks P) {
   using Acc = typename std::conditional<I8, int, float>::type;
-  __shared__ Acc red[kDotWarps][kHeadDotRows * kHeadPick];
+  __shared__ Acc red[WARPS][ROWS * kHeadPick];
   __shared__ int ids[kHeadDotRows];
   wait_for_previous_grid();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t pitch = static_cast<int64_t>(P.D) * (I8 ? 1 : 2);  // a multiple of 16 bytes
-  const int nitems = P.done[1];
+  const int nitems = P.grouped ? P.done[1] : P.N * 32;
   for (int it = blockIdx.x; it < nitems; it += gridDim.x) {
-    const int3 item = P.items[it];
+    const int3 item = P.grouped ? P.items[it] : make_int3(P.pick[it], it, 1);
+    if (item.x < 0) continue;
     __syncthreads();  // the previous item's sums and ids have been read
-    if (threadIdx.x < item.z) ids[threadIdx.x] = P.rows[item.y + threadIdx.x];
+    if (threadIdx.x < item.z) ids[threadIdx.x] = P.grouped ? P.rows[item.y + threadIdx.x] : it;
     __syncthreads();
-    if (item.z <= 16) dot_item<I8, 1, 4>(P, item.x, item.z, ids, red, pitch, lane, w);
-    else dot_item<I8, 4, 1>(P, item.x, item.z, ids, red, pitch, lane, w);
+    if (ROWS <= 16 || item.z <= 16) dot_item<I8, WARPS, 1, 4>(P, item.x, item.z, ids, red[w], pitch, lane, w);
+    else dot_item<I8, WARPS, ROWS / 16, 1>(P, item.x, item.z, ids, red[w], pitch, lane, w);
     __syncthreads();
-    for (int i = threadIdx.x; i < item.z * kHeadPick; i += kDotWarps * 32) {
+    for (int i = threadIdx.x; i < item.z * kHeadPick; i += WARPS * 32) {
       Acc z = 0;
 #pragma unroll
-      for (int k = 0; k < kDotWarps; ++k) z += red[k][i];
+      for (int k = 0; k < WARPS; ++k) z += red[k][i];
       const int p = ids[i / kHeadPick], col = item.x * kHeadPick + i % kHeadPick;
       if (col < P.V) {
         float v = static_cast<float>(z);
@@ -1049,7 +1109,13 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
     const float tol = (F.C8 != nullptr ? 0x1p-21f : 0x1p-15f) * (scale < 3e38f ? scale : 0.f);
     const float before = __shfl_up_sync(0xffffffffu, v, 1);
     const bool close = lane > 0 && mine != 0 && isfinite(v) && isfinite(before) && before - v <= tol;
-    const unsigned joins = __ballot_sync(0xffffffffu, close);  // bit i: i is close to i - 1
+    unsigned joins = __ballot_sync(0xffffffffu, close);  // bit i: i is close to i - 1
+    if (F.top_k < 32) {  // runs that start behind the last alternative do not matter
+      const unsigned behind = joins >> F.top_k;
+      const unsigned reach = ~behind == 0 ? 32u : static_cast<unsigned>(__ffs(static_cast<int>(~behind)) - 1);
+      const unsigned end = F.top_k + reach;
+      if (end < 32) joins &= (1u << end) - 1u;
+    }
     exact[lane] = static_cast<double>(v);
     if (lane == 0) run_mask = joins;
   }
@@ -1157,16 +1223,15 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
 }
 
 template <bool I8, bool OUT>
-cudaError_t launch_one(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool after_kernel,
-                       cudaStream_t s) {
+cudaError_t launch_one(const HeadMaps& M, const HeadArgs& A, bool after_kernel, cudaStream_t s) {
   auto kernel = head_kernel<I8, OUT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if (after_kernel) {
-    e = launch_after_previous(kernel, dim3(A.split.grid), dim3(NUM_THREADS), SMEM_BYTES, s, tmE, tmC, A);
+    e = launch_after_previous(kernel, dim3(A.split.grid), dim3(NUM_THREADS), SMEM_BYTES, s, M.E, M.C, M.C64, A);
     if (e != cudaSuccess) return e;
   } else {
-    kernel<<<A.split.grid, NUM_THREADS, SMEM_BYTES, s>>>(tmE, tmC, A);
+    kernel<<<A.split.grid, NUM_THREADS, SMEM_BYTES, s>>>(M.E, M.C, M.C64, A);
   }
   note_launches(1);
   return cudaGetLastError();
@@ -1174,28 +1239,34 @@ cudaError_t launch_one(const CUtensorMap& tmE, const CUtensorMap& tmC, const Hea
 
 }  // namespace
 
-cudaError_t launch_head(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool int8, bool after_kernel,
-                        cudaStream_t s) {
-  if (A.out != nullptr) return launch_one<true, true>(tmE, tmC, A, after_kernel, s);
-  if (int8) return launch_one<true, false>(tmE, tmC, A, after_kernel, s);
-  return launch_one<false, false>(tmE, tmC, A, after_kernel, s);
+cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool after_kernel, cudaStream_t s) {
+  if (A.out != nullptr) return launch_one<true, true>(M, A, after_kernel, s);
+  if (int8) return launch_one<true, false>(M, A, after_kernel, s);
+  return launch_one<false, false>(M, A, after_kernel, s);
 }
 
+// Up to this many rows every pick is computed for its row alone: the rows' picks are then nearly all different, and
+// bringing equal ones together costs more (a launch, and a chain of atomics in the one before) than it saves.
+constexpr int kUngroupedRows = 64;
+
 cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s) {
-  // With few rows each gets more warps: a row's picks are then found in a quarter of the time, at the cost of more
-  // insertions, which only full machines feel.
-  const int warps = P.N < 2 * sms ? kPickWarpsMax : 8;
-  P.scatter_here = P.N <= 128 ? 1 : 0;
-  cudaError_t e = launch_after_previous(head_pick_kernel, dim3(P.N), dim3(32 * warps), 0, s, P);
+  P.grouped = P.N > kUngroupedRows ? 1 : 0;
+  // with few rows each gets more warps, as the machine is not full
+  cudaError_t e = P.N < 2 * sms ? launch_after_previous(head_pick_kernel<32>, dim3(P.N), dim3(1024), 0, s, P)
+                                : launch_after_previous(head_pick_kernel<8>, dim3(P.N), dim3(256), 0, s, P);
   if (e != cudaSuccess) return e;
-  if (!P.scatter_here) {
+  if (P.grouped) {
     e = launch_after_previous(head_scatter_kernel, dim3((P.N * 32 + 255) / 256), dim3(256), 0, s, P);
     if (e != cudaSuccess) return e;
+    const dim3 grid(std::min(P.N * 32, 4 * sms));
+    e = int8 ? launch_after_previous(head_dots_kernel<true, 4, kHeadDotRows>, grid, dim3(128), 0, s, P)
+             : launch_after_previous(head_dots_kernel<false, 4, kHeadDotRows>, grid, dim3(128), 0, s, P);
+  } else {
+    const dim3 grid(std::min(P.N * 32, 2 * sms));
+    e = int8 ? launch_after_previous(head_dots_kernel<true, 8, 16>, grid, dim3(256), 0, s, P)
+             : launch_after_previous(head_dots_kernel<false, 8, 16>, grid, dim3(256), 0, s, P);
   }
-  const dim3 grid(std::min(P.N * 32, 2 * sms)), block(kDotWarps * 32);
-  e = int8 ? launch_after_previous(head_dots_kernel<true>, grid, block, 0, s, P)
-           : launch_after_previous(head_dots_kernel<false>, grid, block, 0, s, P);
-  note_launches(P.scatter_here ? 2 : 3);
+  note_launches(P.grouped ? 3 : 2);
   return e;
 }
 

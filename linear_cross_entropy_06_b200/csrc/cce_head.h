@@ -12,6 +12,7 @@ namespace cce {
 
 constexpr int kHeadBM = 128;       // rows of a logit tile
 constexpr int kHeadBN = 256;       // vocabulary columns of a logit tile
+constexpr int kHeadUnit = 64;      // smallest unit of the split
 constexpr int kHeadGroup = 32;     // row blocks that walk the vocabulary together (their E stays in L2)
 constexpr int kHeadMaxTokens = 32; // given tokens a row
 constexpr int kHeadMaxTop = 24;    // alternatives a row
@@ -63,7 +64,6 @@ struct HeadArgs {
   int N, D, V;
   int num_kb;    // K-blocks of 128 bytes
   int kb_chunk;  // K-blocks summed in one tensor-memory accumulator
-  int box_c;     // rows of C a TMA box
   int e_rows;    // rows of E a TMA box
   const __nv_bfloat16* bias;  // [V] or null
   const float* e_scale;       // [N], [V]: scales of 8-bit operands
@@ -99,7 +99,7 @@ struct HeadPicks {
   const float* pick_max;  // [N, picks]
   int picks;
   int wanted;       // picks a row, at most 32
-  int scatter_here;
+  int grouped;      // whether equal picks of several rows are brought together
   int* done;        // [2]: blocks done (zero before), work items
   int* count;       // [picks], zero before: rows that want the pick
   int* base;        // [picks]: their place in rows
@@ -108,6 +108,12 @@ struct HeadPicks {
   int* rows;        // [32 N]: 32 row + j
   int3* items;      // [32 N]: pick, first of its rows, how many
   float* logits;    // [N, 32, 16]
+};
+
+struct HeadMaps {
+  CUtensorMap E;    // box of e_rows rows x 128 bytes
+  CUtensorMap C;    // box of 256 rows
+  CUtensorMap C64;  // box of 64 rows
 };
 
 struct HeadFinish {
@@ -141,8 +147,7 @@ struct HeadFinish {
   const int* failed;
 };
 
-cudaError_t launch_head(const CUtensorMap& tmE, const CUtensorMap& tmC, const HeadArgs& A, bool int8, bool after_kernel,
-                        cudaStream_t s);
+cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool after_kernel, cudaStream_t s);
 // These two follow a kernel of the same call on s.
 cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s);
 cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s);

@@ -7,7 +7,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
-#include <numeric>
 
 #include "cce.h"
 #include "cce_head.h"
@@ -59,30 +58,49 @@ bool logprobs_ok(const cce_logprob_problem* p, bool set_error) {
   return true;
 }
 
-// The split of the logit tiles over `sms` blocks. With at least kWideTiles tiles a block, units of a whole tile:
-// one load a stage brings 256 rows of C, and a block's share is uneven by at most one tile in that many. With fewer,
-// units of 64 columns, loaded 64 rows at a time, so that the blocks' shares of C stay even: one row block of 128256
-// columns on 148 SMs gets 13.5 units (at most 14) instead of 3.4 tiles (at most 4).
+// The split of the logit tiles over `sms` blocks. With at least kWideTiles tiles a block, units of a whole tile: a
+// block's share is uneven by at most one tile in that many, and the walk can be aligned. With fewer, units of 64
+// columns, so that the blocks' shares of C stay even: one row block of 128256 columns on 148 SMs gets 13.5 units (at
+// most 14) instead of 3.4 tiles (at most 4).
 constexpr int64_t kWideTiles = 12;
+constexpr int kEvenPercent = 94;
 
 cce::HeadSplit make_split(int64_t N, int64_t V, int sms) {
-  cce::HeadSplit S{};
+  cce::HeadSplit S;
   S.nb = static_cast<int>(ceil_div(N, cce::kHeadBM));
   S.ngroups = static_cast<int>(ceil_div(S.nb, cce::kHeadGroup));
   S.grid = sms;
   const int64_t rows = std::max<int64_t>(S.nb / std::max(S.ngroups, 1), 1);
-  S.unit = rows * ceil_div(V, cce::kHeadBN) >= kWideTiles * sms ? cce::kHeadBN : 64;
+  const bool wide = rows * ceil_div(V, cce::kHeadBN) >= kWideTiles * sms;
+  S.unit = wide ? cce::kHeadBN : cce::kHeadUnit;
   S.nu = static_cast<int>(ceil_div(V, S.unit));
-  for (int k = 0; k < 2; ++k) {
-    const int total = S.units(static_cast<int>(rows) + k), P = S.parts(total);
-    int parts[cce::kHeadMaxGrid];
-    std::iota(parts, parts + P, 0);
-    std::stable_sort(parts, parts + P, [&](int a, int b) {
-      return cce::HeadSplit::part_begin(a, total, P) % S.nu < cce::HeadSplit::part_begin(b, total, P) % S.nu;
-    });
-    for (int i = 0; i < P; ++i) S.order[k][i] = static_cast<uint8_t>(parts[i]);
+  // Small problems: the same number of parts for every row block, where that leaves few SMs idle. The row blocks'
+  // parts then start at the same columns, and each column of C is read from HBM once (777 x 1288 x 50257: 138 us
+  // against 173 with even shares for all SMs). With wide units the walk itself is aligned (for_tiles), and idle SMs
+  // cost more than that leaves to gain (2048 x 2048 x 128256: 906 us against 889 on the same machine).
+  if (!wide && S.ngroups == 1) {
+    const int even = sms / S.nb * S.nb;
+    if (even * 100 >= kEvenPercent * sms) S.grid = even;
   }
   return S;
+}
+
+// Parts by where they start in the vocabulary: counted into 256 equal stretches of it (nearer than that their order
+// does not matter).
+void order_parts(cce::HeadSplit* S) {
+  for (int k = 0; k < 2; ++k) {
+    const int total = S->units(S->nb / S->ngroups + k), P = S->parts(total);
+    uint8_t stretch[cce::kHeadMaxGrid];
+    int place[257] = {};
+    for (int i = 0; i < P; ++i) {
+      const int64_t start = cce::HeadSplit::part_begin(i, total, P) % S->nu;
+      stretch[i] = static_cast<uint8_t>(start * 256 / S->nu);
+      ++place[stretch[i] + 1];
+    }
+    for (int i = 0; i < 256; ++i) place[i + 1] += place[i];
+    for (int i = 0; i < P; ++i) S->order[k][place[stretch[i]]++] = static_cast<uint8_t>(i);
+    if (S->nb % S->ngroups == 0) break;  // every group has the same number of row blocks
+  }
 }
 
 constexpr int kMaxSms = cce::kHeadMaxGrid;  // the workspace is sized for it; a device with fewer SMs needs no more
@@ -163,15 +181,15 @@ HeadWs carve(int64_t N, int64_t D, int64_t V, int K, int top_k, bool int8, bool 
 // The arguments and tensor maps that every head launch shares; E and e_scale: the operand's own rows.
 cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, const float* e_scale, const void* C,
                      const void* bias, const float* c_scale, const HeadWs& w, int sms, cce::HeadArgs* A,
-                     CUtensorMap* tmE, CUtensorMap* tmC) {
+                     cce::HeadMaps* M) {
   A->split = make_split(N, V, std::min(sms, kMaxSms));
+  order_parts(&A->split);
   A->N = static_cast<int>(N);
   A->D = static_cast<int>(D);
   A->V = static_cast<int>(V);
   const int per_block = int8 ? 128 : 64;  // values of a 128-byte K-block
   A->num_kb = static_cast<int>(ceil_div(D, per_block));
   A->kb_chunk = int8 ? A->num_kb : kChunkBlocks;
-  A->box_c = A->split.unit;
   A->e_rows = static_cast<int>(std::min<int64_t>(cce::kHeadBM, (N + 7) / 8 * 8));
   A->bias = static_cast<const __nv_bfloat16*>(bias);
   A->e_scale = e_scale;
@@ -185,8 +203,9 @@ cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, 
   A->inject_stall = (stall != nullptr && stall[0] == '4') ? 1 : 0;
   const auto type = int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const size_t size = int8 ? 1 : 2;
-  CCE_CHECK(cce::make_map(tmE, type, size, E, N, D, per_block, static_cast<uint32_t>(A->e_rows)));
-  CCE_CHECK(cce::make_map(tmC, type, size, C, V, D, per_block, static_cast<uint32_t>(A->box_c)));
+  CCE_CHECK(cce::make_map(&M->E, type, size, E, N, D, per_block, static_cast<uint32_t>(A->e_rows)));
+  CCE_CHECK(cce::make_map(&M->C, type, size, C, V, D, per_block, cce::kHeadBN));
+  CCE_CHECK(cce::make_map(&M->C64, type, size, C, V, D, per_block, cce::kHeadUnit));
   return CCE_OK;
 }
 
@@ -252,8 +271,8 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     if (K > 1) CCE_TRY(cce::launch_head_tokens(tok, static_cast<int>(n), K, static_cast<int>(p->V), p->ignore_index,
                                                w.tok_t, s));
     cce::HeadArgs A{};
-    CUtensorMap tmE, tmC;
-    CCE_CHECK(head_args(n, p->D, p->V, int8, operand, e_scale, C, bias, c_scale, w, sms, &A, &tmE, &tmC));
+    cce::HeadMaps M;
+    CCE_CHECK(head_args(n, p->D, p->V, int8, operand, e_scale, C, bias, c_scale, w, sms, &A, &M));
     A.tokens = tok;
     A.tok_t = w.tok_t;
     A.ignore_index = p->ignore_index;
@@ -267,7 +286,7 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     A.part_s = w.part_s;
     A.part_w = w.part_w;
     // it follows a kernel directly where the operands or the tokens were prepared on the stream
-    CCE_TRY(cce::launch_head(tmE, tmC, A, int8, K > 1 || (int8 && r0 == 0), s));
+    CCE_TRY(cce::launch_head(M, A, int8, K > 1 || (int8 && r0 == 0), s));
 
     cce::HeadPicks P{};
     if (top_k > 0) {
@@ -410,12 +429,12 @@ cce_status cce_int8_linear(int64_t N, int64_t D, int64_t V, const void* E, const
   if (N == 0) return CCE_OK;
   CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), N, D, w.e8, w.e_scale, s));
   cce::HeadArgs A{};
-  CUtensorMap tmE, tmC;
-  CCE_CHECK(head_args(N, D, V, true, w.e8, w.e_scale, C, bias, c_scale, w, sms, &A, &tmE, &tmC));
+  cce::HeadMaps M;
+  CCE_CHECK(head_args(N, D, V, true, w.e8, w.e_scale, C, bias, c_scale, w, sms, &A, &M));
   A.inv_t = 1.f;
   A.out = out;
   A.out_fp32 = out_fp32;
-  CCE_TRY(cce::launch_head(tmE, tmC, A, true, true, s));
+  CCE_TRY(cce::launch_head(M, A, true, true, s));
   return CCE_OK;
 }
 

@@ -200,6 +200,7 @@ struct BwdArgs {
   const float* lp_tok_g;  // [lp_k, N]
   int lp_k;
   float lp_inv_t;         // 1 / temperature
+  int de_split;           // dE items a row block, slice and chunk: each adds its share of the row block's tiles
 };
 
 struct BwdLaunch {
@@ -238,6 +239,7 @@ struct PlanArgs {
   uint64_t timeout_ns;
   const int* tok;          // [K, N] given tokens (-1: none) whose units are always kept, or null
   int K;
+  int de_split;            // BwdArgs.de_split (a plan that skips has 1)
   int inject_stall;        // test hook: block 0 leaves before the first grid barrier, whose wait then runs out
 };
 // One cooperative launch: the row scales, the tile flags, both tile lists, the quad list, the
@@ -274,7 +276,7 @@ struct BwdFinalize {
 // dC rows of the vocabulary tiles no row block lists.
 cudaError_t launch_empty_tiles(const BwdFinalize& F, int num_sms, bool after_kernel, cudaStream_t s);
 // dE's last terms and conversion, dbias (after the tensor-core kernel and launch_empty_tiles).
-cudaError_t launch_bwd_finalize(const BwdFinalize& F, int num_sms, cudaStream_t s);
+cudaError_t launch_bwd_finalize(const BwdFinalize& F, int num_sms, bool after_kernel, cudaStream_t s);
 // out[b * T + j] = 1 if half j of row block b was skipped, 0 if it was kept (b < nb, j < T).
 cudaError_t launch_skip_map(const uint8_t* flags, int nb, int nt, int64_t T, uint8_t* out, cudaStream_t s);
 
@@ -317,7 +319,7 @@ cudaError_t launch_shard_merge(const float* partials, int shards, const int64_t*
                                float* lse, int64_t* count, cudaStream_t s);
 cudaError_t launch_fill_zero(void* dst, int64_t bytes, cudaStream_t s);
 
-// What the backward of the log-probabilities needs before its plan (cce_aux.cu, one launch). With
+// What the backward of the log-probabilities needs before its plan (cce_bwd_plan.cu, one launch). With
 // y = z / T, lp_k = y_{t_k} - lse, p = softmax(y) and the gradients g_k of lp_k and h of the entropy H:
 //   dz_v = (1 / T) (sum_k g_k [v = t_k] - p_v (sum_k g_k + h H + h ln p_v)).
 // Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and tok_g[k] = g_k / T for the tokens
@@ -343,6 +345,7 @@ struct LogprobPrep {
   float* one;               // [1] 1.0: the scale of every row's gradient
   __nv_bfloat16* E_out;     // [N, D]
 };
-cudaError_t launch_logprob_prep(const LogprobPrep& P, cudaStream_t s);
+// With A.filter_on = 0 it lays out the plan of A as well (every tile kept), and no launch_bwd_plan follows.
+cudaError_t launch_logprob_prep(const LogprobPrep& P, const PlanArgs& A, int num_sms, cudaStream_t s);
 
 }  // namespace cce

@@ -16,6 +16,7 @@ before a pointer reaches the library, and there is no CPU path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import NamedTuple, Optional, Tuple, Union
@@ -23,7 +24,7 @@ from typing import NamedTuple, Optional, Tuple, Union
 import torch
 
 from . import ops
-from .ops import _bias_arg, _check, _ptr, _require, _require_cuda, _stream
+from .ops import _bias_arg, _check, _ptr, _require_cuda, _stream
 
 MAX_TOKENS = 32  # given tokens a position
 MAX_TOP = 24     # alternatives a position
@@ -50,28 +51,53 @@ class TopLogprobs(NamedTuple):
 Classifier = Union[torch.Tensor, Int8Rows]
 
 
+def _refuse(message: str) -> None:
+    raise ops.CCEError(1, message)
+
+
 def _check_classifier(c: Classifier, D: int) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """The classifier's rows [V, D] and, for 8-bit ones, their scales."""
     if isinstance(c, Int8Rows):
-        values, scale = c
-        _require(values.dtype == torch.int8 and values.dim() == 2,
-                 f"Int8Rows.values must be int8 [V, D], got {values.dtype} {tuple(values.shape)}")
-        _require(scale.dtype == torch.float32 and scale.numel() == values.shape[0],
-                 f"Int8Rows.scale must be float32 with {values.shape[0]} entries, got {scale.dtype} {tuple(scale.shape)}")
-        _require(D % 16 == 0, f"D must be a multiple of 16 for 8-bit operands, got {D}")
-        rows = values
+        rows, scale = c
+        if rows.dtype != torch.int8 or rows.dim() != 2:
+            _refuse(f"Int8Rows.values must be int8 [V, D], got {rows.dtype} {tuple(rows.shape)}")
+        if scale.dtype != torch.float32 or scale.numel() != rows.shape[0]:
+            _refuse(f"Int8Rows.scale must be float32 with {rows.shape[0]} entries, got {scale.dtype} "
+                    f"{tuple(scale.shape)}")
+        if D % 16 != 0:
+            _refuse(f"D must be a multiple of 16 for 8-bit operands, got {D}")
     else:
-        _require(c.dim() == 2, f"c must be 2-D, got {tuple(c.shape)}")
-        _require(c.dtype == torch.bfloat16, f"c must be bfloat16 or Int8Rows, got {c.dtype}")
         rows, scale = c, None
-    _require(rows.shape[1] == D, f"c must be [V, {D}], got {tuple(rows.shape)}")
+        if rows.dim() != 2:
+            _refuse(f"c must be 2-D, got {tuple(rows.shape)}")
+        if rows.dtype != torch.bfloat16:
+            _refuse(f"c must be bfloat16 or Int8Rows, got {rows.dtype}")
+    if rows.shape[1] != D:
+        _refuse(f"c must be [V, {D}], got {tuple(rows.shape)}")
     return rows, scale
 
 
 def _flat(e: torch.Tensor) -> torch.Tensor:
-    _require(e.dim() >= 1, "e must have a last dimension of size D")
-    _require(e.dtype == torch.bfloat16, f"e must be bfloat16, got {e.dtype}")
-    return e.reshape(-1, e.shape[-1])
+    if e.dim() < 1:
+        _refuse("e must have a last dimension of size D")
+    if e.dtype != torch.bfloat16:
+        _refuse(f"e must be bfloat16, got {e.dtype}")
+    return e if e.dim() == 2 else e.reshape(-1, e.shape[-1])
+
+
+def _check_matrix(E: torch.Tensor) -> Tuple[int, int]:
+    if E.dim() != 2 or E.dtype != torch.bfloat16:
+        _refuse(f"E must be bfloat16 [N, D], got {E.dtype} {tuple(E.shape)}")
+    return E.shape
+
+
+def _check_tokens(tokens: torch.Tensor, N: int) -> int:
+    if tokens.dtype != torch.int64 or tokens.dim() != 2 or tokens.shape[0] != N:
+        _refuse(f"tokens must be int64 [{N}, K], got {tokens.dtype} {tuple(tokens.shape)}")
+    K = tokens.shape[1]
+    if not 1 <= K <= MAX_TOKENS:
+        _refuse(f"1 to {MAX_TOKENS} tokens a position, got {K}")
+    return K
 
 
 def _aligned(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
@@ -79,13 +105,9 @@ def _aligned(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     buffer may begin anywhere: it is copied then)."""
     if t is None:
         return None
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
-
-
-def _problem(N: int, D: int, V: int, ignore_index: int, tokens: int, top_k: int, temperature: float,
-             int8: bool) -> ops.LogprobProblem:
-    return ops.LogprobProblem(N, D, V, ignore_index, tokens, top_k, temperature, int(int8), 0)
 
 
 def _check_scalars(top_k: int, V: int, temperature: float) -> None:
@@ -93,6 +115,11 @@ def _check_scalars(top_k: int, V: int, temperature: float) -> None:
         raise ValueError(f"temperature must be finite and > 0, got {temperature}")
     if not 0 <= top_k <= min(MAX_TOP, V):
         raise ValueError(f"the number of alternatives must be in [0, {min(MAX_TOP, V)}], got {top_k}")
+
+
+def _on(dev: torch.device):
+    """The device of a call as the current one (entering the context costs more than looking)."""
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor], top_k: int = 0,
@@ -103,36 +130,33 @@ def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor],
     three are None without tokens, the last two without alternatives. ``save_max`` keeps what a backward
     that skips units needs."""
     lib = ops.load_library()
-    _require(E.dim() == 2, f"E must be 2-D, got {tuple(E.shape)}")
-    E = _flat(E)
-    N, D = E.shape
+    N, D = _check_matrix(E)
     rows, scale = _check_classifier(C, D)
     V = rows.shape[0]
     _check_scalars(top_k, V, temperature)
-    K = 0
-    if tokens is not None:
-        _require(tokens.dtype == torch.int64, f"tokens must be int64, got {tokens.dtype}")
-        _require(tokens.dim() == 2 and tokens.shape[0] == N, f"tokens must be [{N}, K], got {tuple(tokens.shape)}")
-        K = tokens.shape[1]
-        _require(1 <= K <= MAX_TOKENS, f"1 to {MAX_TOKENS} tokens a position, got {K}")
-    dev = _require_cuda(E, rows, *(t for t in (scale, tokens) if t is not None))
+    K = 0 if tokens is None else _check_tokens(tokens, N)
+    dev = _require_cuda(*(t for t in (E, rows, scale, tokens) if t is not None))
     E, rows, scale, bias = _aligned(E), _aligned(rows), _aligned(scale), _aligned(_bias_arg(bias, V, dev))
     tokens = None if tokens is None else tokens.contiguous()
-    p = _problem(N, D, V, ignore_index, K, top_k, temperature, scale is not None)
-    ws_bytes = lib.cce_logprobs_workspace_size(ctypes.byref(p))
-    _require(ws_bytes > 0, f"bad problem N={N} D={D} V={V} tokens={K} top_k={top_k}")
-
-    def empty(*shape, dtype=torch.float32):
-        return torch.empty(*shape, device=dev, dtype=dtype)
-
-    logprobs, entropy, lse = (empty(N, K), empty(N), empty(N)) if K else (None, None, None)
-    tile_max = empty(max(-(-V // 64) * N, 1)) if save_max else None
-    top_lp, top_ids = (empty(N, top_k), empty(N, top_k, dtype=torch.int64)) if top_k else (None, None)
-    ws = empty(ws_bytes, dtype=torch.uint8)
-    with torch.cuda.device(dev):
-        _check(lib.cce_logprobs(ctypes.byref(p), _ptr(E), _ptr(rows), _ptr(scale), _ptr(bias), _ptr(tokens),
+    p = ctypes.byref(ops.LogprobProblem(N, D, V, ignore_index, K, top_k, temperature, scale is not None, 0))
+    ws_bytes = lib.cce_logprobs_workspace_size(p)
+    if ws_bytes == 0:
+        _refuse(f"bad problem N={N} D={D} V={V} tokens={K} top_k={top_k} ignore_index={ignore_index}")
+    logprobs = entropy = lse = tile_max = top_lp = top_ids = None
+    if K:
+        logprobs = torch.empty(N, K, device=dev, dtype=torch.float32)
+        entropy = torch.empty(N, device=dev, dtype=torch.float32)
+        lse = torch.empty(N, device=dev, dtype=torch.float32)
+    if save_max:
+        tile_max = torch.empty(max(-(-V // 64) * N, 1), device=dev, dtype=torch.float32)
+    if top_k:
+        top_lp = torch.empty(N, top_k, device=dev, dtype=torch.float32)
+        top_ids = torch.empty(N, top_k, device=dev, dtype=torch.int64)
+    ws = torch.empty(ws_bytes, device=dev, dtype=torch.uint8)
+    with _on(dev):
+        _check(lib.cce_logprobs(p, E.data_ptr(), rows.data_ptr(), _ptr(scale), _ptr(bias), _ptr(tokens),
                                 _ptr(logprobs), _ptr(entropy), _ptr(lse), _ptr(tile_max), _ptr(top_lp), _ptr(top_ids),
-                                _ptr(ws), ws_bytes, _stream(dev)))
+                                ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
     return logprobs, entropy, lse, tile_max, top_lp, top_ids
@@ -147,26 +171,24 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     """Run the backward of ``cce_logprobs``. Returns (dE, dC, filtered_tiles) as device tensors, then
     dbias when it is computed (by default whenever ``bias`` is given)."""
     lib = ops.load_library()
-    _require(E.dim() == 2, f"E must be 2-D, got {tuple(E.shape)}")
-    E = _flat(E)
-    N, D = E.shape
-    _require(isinstance(C, torch.Tensor), "a classifier of 8-bit integers has no gradient")
+    N, D = _check_matrix(E)
+    if isinstance(C, Int8Rows):
+        _refuse("a classifier of 8-bit integers has no gradient")
     rows, _ = _check_classifier(C, D)
     V = rows.shape[0]
     _check_scalars(0, V, temperature)
-    _require(tokens.dtype == torch.int64 and tokens.dim() == 2 and tokens.shape[0] == N,
-             f"tokens must be int64 [{N}, K], got {tokens.dtype} {tuple(tokens.shape)}")
-    K = tokens.shape[1]
-    _require(1 <= K <= MAX_TOKENS, f"1 to {MAX_TOKENS} tokens a position, got {K}")
+    K = _check_tokens(tokens, N)
     for name, t, n in (("lse", lse, N), ("entropy", entropy, N), ("grad_logprobs", grad_logprobs, N * K),
                        ("grad_entropy", grad_entropy, N)):
-        _require(t is None or (t.dtype == torch.float32 and t.numel() == n), f"{name} must be float32 with {n} entries")
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n):
+            _refuse(f"{name} must be float32 with {n} entries, got {t.dtype} {tuple(t.shape)}")
     if filter_eps > 0.0:
         need = -(-V // 64) * N
-        _require(tile_max is not None and tile_max.dtype == torch.float32 and tile_max.numel() >= need,
-                 f"filter_eps > 0 needs tile_max, float32 with at least {need} entries")
+        if tile_max is None or tile_max.dtype != torch.float32 or tile_max.numel() < need:
+            _refuse(f"filter_eps > 0 needs tile_max, float32 with at least {need} entries")
     mode = int(out_fp32)
-    _require(mode in (ops.OUT_BF16, ops.OUT_FP32, ops.OUT_DE_FP32), f"out_fp32 must be 0, 1 or 2, got {out_fp32!r}")
+    if mode not in (ops.OUT_BF16, ops.OUT_FP32, ops.OUT_DE_FP32):
+        _refuse(f"out_fp32 must be 0, 1 or 2, got {out_fp32!r}")
     dev = _require_cuda(*(t for t in (E, rows, tokens, lse, entropy, tile_max, grad_logprobs, grad_entropy)
                           if t is not None))
     E, rows, bias = _aligned(E), _aligned(rows), _aligned(_bias_arg(bias, V, dev))
@@ -175,9 +197,10 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     g_h = None if grad_entropy is None else grad_entropy.contiguous()
     tile_max = None if tile_max is None else tile_max.contiguous()
     want_dbias = (bias is not None) if dbias is None else bool(dbias)
-    p = _problem(N, D, V, ignore_index, K, 0, temperature, False)
-    ws_bytes = lib.cce_logprobs_backward_workspace_size(ctypes.byref(p), mode)
-    _require(ws_bytes > 0, f"bad problem: {lib.cce_last_error_message().decode()}")
+    p = ctypes.byref(ops.LogprobProblem(N, D, V, ignore_index, K, 0, temperature, 0, 0))
+    ws_bytes = lib.cce_logprobs_backward_workspace_size(p, mode)
+    if ws_bytes == 0:
+        _refuse(f"bad problem: {lib.cce_last_error_message().decode()}")
     de_dtype = torch.float32 if mode in (ops.OUT_FP32, ops.OUT_DE_FP32) else torch.bfloat16
     dc_dtype = torch.float32 if mode == ops.OUT_FP32 else torch.bfloat16
     dE = torch.empty(N, D, device=dev, dtype=de_dtype)
@@ -185,11 +208,11 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     db = torch.empty(V, device=dev, dtype=dc_dtype) if want_dbias else None
     filtered = torch.empty(1, device=dev, dtype=torch.int64)
     ws = torch.empty(ws_bytes, device=dev, dtype=torch.uint8)
-    with torch.cuda.device(dev):
-        _check(lib.cce_logprobs_backward(ctypes.byref(p), _ptr(E), _ptr(rows), _ptr(bias), _ptr(tokens), _ptr(lse),
-                                         _ptr(entropy), _ptr(tile_max), _ptr(g_lp), _ptr(g_h), float(filter_eps),
-                                         _ptr(dE), _ptr(dC), _ptr(db), mode, _ptr(filtered), _ptr(ws), ws_bytes,
-                                         _stream(dev)))
+    with _on(dev):
+        _check(lib.cce_logprobs_backward(p, E.data_ptr(), rows.data_ptr(), _ptr(bias), tokens.data_ptr(),
+                                         lse.data_ptr(), entropy.data_ptr(), _ptr(tile_max), _ptr(g_lp), _ptr(g_h),
+                                         float(filter_eps), dE.data_ptr(), dC.data_ptr(), _ptr(db), mode,
+                                         filtered.data_ptr(), ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
     return (dE, dC, filtered) + ((db,) if want_dbias else ())
@@ -251,24 +274,31 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
             raise ValueError("shift needs one token a position and a sequence axis of length >= 1")
         tokens = ops.shift_targets(tokens, ignore_index)
     E = _flat(e)
-    t = tokens.to(torch.int64).reshape(E.shape[0], -1) if E.shape[0] else \
-        tokens.to(torch.int64).reshape(0, tokens.shape[-1] if many else 1)
-    if isinstance(c, Int8Rows):
-        if torch.is_grad_enabled() and (e.requires_grad or (bias is not None and bias.requires_grad)):
-            raise ValueError("a classifier of 8-bit integers has no gradient: call under torch.no_grad(), or detach e "
-                             "and bias")
+    t = tokens.to(torch.int64)
+    if not many:
+        t = t.reshape(-1, 1)
+    elif t.dim() != 2:
+        t = t.reshape(-1, t.shape[-1])
+    grad = torch.is_grad_enabled() and (e.requires_grad or (bias is not None and bias.requires_grad) or
+                                        (isinstance(c, torch.Tensor) and c.requires_grad))
+    if not grad:
         logprobs, entropy, _, _, top_lp, top_ids = cce_logprobs(E, c, t, top_k, bias, temperature, ignore_index)
+    elif isinstance(c, Int8Rows):
+        raise ValueError("a classifier of 8-bit integers has no gradient: call under torch.no_grad(), or detach e and "
+                         "bias")
     else:
         logprobs, entropy, top_lp, top_ids = _LinearLogprobs.apply(E, c, bias, t, int(top_k), float(temperature),
                                                                    ignore_index, float(filter_eps))
-    out = Logprobs(logprobs.reshape(tokens.shape), entropy.reshape(lead),
-                   None if top_lp is None else top_lp.reshape(*lead, top_k),
-                   None if top_ids is None else top_ids.reshape(*lead, top_k))
-    if not shift:
-        return out
-    return Logprobs(out.logprobs[..., :-1], out.entropy[..., :-1],
-                    None if top_lp is None else out.top_logprobs[..., :-1, :],
-                    None if top_ids is None else out.top_ids[..., :-1, :])
+    logprobs = logprobs.reshape(tokens.shape)
+    if len(lead) != 1:
+        entropy = entropy.reshape(lead)
+        if top_k:
+            top_lp, top_ids = top_lp.reshape(*lead, top_k), top_ids.reshape(*lead, top_k)
+    if shift:
+        logprobs, entropy = logprobs[..., :-1], entropy[..., :-1]
+        if top_k:
+            top_lp, top_ids = top_lp[..., :-1, :], top_ids[..., :-1, :]
+    return Logprobs(logprobs, entropy, top_lp, top_ids)
 
 
 def linear_top_logprobs(e: torch.Tensor, c: Classifier, k: int, bias: Optional[torch.Tensor] = None,
@@ -281,10 +311,10 @@ def linear_top_logprobs(e: torch.Tensor, c: Classifier, k: int, bias: Optional[t
     """
     if k < 1:
         raise ValueError(f"k must be at least 1, got {k}")
-    with torch.no_grad():
-        E = _flat(e)
-        out = cce_logprobs(E, c, None, int(k), bias, float(temperature))
+    out = cce_logprobs(_flat(e), c, None, k, bias, temperature)
     lead = e.shape[:-1]
+    if len(lead) == 1:
+        return TopLogprobs(out[4], out[5])
     return TopLogprobs(out[4].reshape(*lead, k), out[5].reshape(*lead, k))
 
 
@@ -293,13 +323,15 @@ def quantize_int8(x: torch.Tensor) -> Int8Rows:
     values = x / scale, rounded to the nearest integer, halves to the even one. D must be a multiple of
     16. A row of zeros gets scale 0; a row that holds an infinity or a NaN gets the scale NaN."""
     lib = ops.load_library()
-    _require(x.dim() == 2 and x.dtype == torch.bfloat16, f"x must be bfloat16 [rows, D], got {x.dtype} {tuple(x.shape)}")
-    _require(x.shape[1] >= 16 and x.shape[1] % 16 == 0, f"D must be a positive multiple of 16, got {x.shape[1]}")
+    if x.dim() != 2 or x.dtype != torch.bfloat16:
+        _refuse(f"x must be bfloat16 [rows, D], got {x.dtype} {tuple(x.shape)}")
+    if x.shape[1] < 16 or x.shape[1] % 16 != 0:
+        _refuse(f"D must be a positive multiple of 16, got {x.shape[1]}")
     dev = _require_cuda(x)
     x = _aligned(x.detach())
     out = Int8Rows(torch.empty(x.shape, device=dev, dtype=torch.int8),
                    torch.empty(x.shape[0], device=dev, dtype=torch.float32))
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.cce_quantize_int8(_ptr(x), x.shape[0], x.shape[1], _ptr(out.values), _ptr(out.scale), _stream(dev)))
     return out
 
@@ -311,22 +343,24 @@ def int8_linear(e: torch.Tensor, c: Int8Rows, bias: Optional[torch.Tensor] = Non
     Each row of e (bf16) is rounded to 8-bit integers with a scale of its own, the sums of integer
     products are exact, and the two scales and the bias are applied in fp32. No gradient flows."""
     lib = ops.load_library()
-    _require(isinstance(c, Int8Rows), f"c must be Int8Rows (see quantize_int8), got {type(c).__name__}")
-    _require(out_dtype in (torch.bfloat16, torch.float32), f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-    E = _flat(e).detach()
+    if not isinstance(c, Int8Rows):
+        _refuse(f"c must be Int8Rows (see quantize_int8), got {type(c).__name__}")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        _refuse(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    E = _flat(e)
     N, D = E.shape
     rows, scale = _check_classifier(c, D)
     V = rows.shape[0]
     dev = _require_cuda(E, rows, scale)
-    E, rows, scale = _aligned(E), _aligned(rows), _aligned(scale)
-    bias = _aligned(_bias_arg(None if bias is None else bias.detach(), V, dev))
+    E, rows, scale, bias = _aligned(E), _aligned(rows), _aligned(scale), _aligned(_bias_arg(bias, V, dev))
     ws_bytes = lib.cce_int8_linear_workspace_size(N, D, V)
-    _require(ws_bytes > 0, f"bad problem N={N} D={D} V={V}")
+    if ws_bytes == 0:
+        _refuse(f"bad problem N={N} D={D} V={V}")
     out = torch.empty(N, V, device=dev, dtype=out_dtype)
     ws = torch.empty(ws_bytes, device=dev, dtype=torch.uint8)
-    with torch.cuda.device(dev):
-        _check(lib.cce_int8_linear(N, D, V, _ptr(E), _ptr(rows), _ptr(scale), _ptr(bias), _ptr(out),
-                                   int(out_dtype == torch.float32), _ptr(ws), ws_bytes, _stream(dev)))
+    with _on(dev):
+        _check(lib.cce_int8_linear(N, D, V, E.data_ptr(), rows.data_ptr(), scale.data_ptr(), _ptr(bias),
+                                   out.data_ptr(), out_dtype == torch.float32, ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
-    return out.reshape(*e.shape[:-1], V)
+    return out if e.dim() == 2 else out.reshape(*e.shape[:-1], V)
