@@ -307,13 +307,13 @@ CCE_API size_t cce_logprobs_backward_workspace_size(const cce_logprob_problem* p
  * Gradients of sum_k g_k logprob_k + h entropy for E, C and bias, with grad_logprobs g device fp32
  * [N, num_tokens] and grad_entropy h device fp32 [N] (either may be NULL: zeros):
  *   dz_v = (sum_k g_k [v = t_k] - p_v (sum_k g_k + h (ln p_v + entropy))) / temperature.
- * lse and entropy as cce_logprobs() returned them. filter_eps > 0 skips units of 128 rows x 64 columns
+ * logprobs, lse and entropy as cce_logprobs() returned them. filter_eps > 0 skips units of 128 rows x 64 columns
  * as cce_backward() does, except those that hold a given token (tile_max is then needed); 0 keeps all.
  * dE, dC, dbias, out_fp32 and filtered_tiles as for cce_backward().
  */
 CCE_API cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, const void* C, const void* bias,
-                                         const int64_t* tokens, const float* lse, const float* entropy,
-                                         const float* tile_max, const float* grad_logprobs, const float* grad_entropy,
+                                         const int64_t* tokens, const float* logprobs, const float* lse,
+                                         const float* entropy, const float* tile_max, const float* grad_logprobs, const float* grad_entropy,
                                          float filter_eps, void* dE, void* dC, void* dbias, int32_t out_fp32,
                                          int64_t* filtered_tiles, void* workspace, size_t workspace_bytes,
                                          cce_stream_t stream);

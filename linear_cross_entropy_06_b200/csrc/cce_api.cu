@@ -312,6 +312,7 @@ LogprobWs carve_logprob(const cce_problem* p, int K, size_t off, void* base) {
   w.prep.coef = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.coef_log = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.lse = reinterpret_cast<float*>(take(sizeof(float) * n));
+  w.prep.row_scale = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.tok = reinterpret_cast<int*>(take(sizeof(int) * n * k));
   w.prep.tok_g = reinterpret_cast<float*>(take(sizeof(float) * n * k));
   w.prep.targets = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * n));
@@ -324,8 +325,8 @@ LogprobWs carve_logprob(const cce_problem* p, int K, size_t off, void* base) {
 // The backward: plan the tiles and work lists, then one persistent launch (cce_bwd.cu) forms the
 // gradient tiles chunk by chunk and runs the dC and dE MMAs from them. With `lp`, of the
 // log-probabilities: the rows' coefficients and the tokens come from logprob_prep_kernel, which also
-// copies E with the rows that ask for nothing zeroed, so that what stands in them (padding, NaN)
-// reaches no product. The plan then sees rows that are scored but have no target of their own (id V of
+// makes the rows of E that dC is formed from, zero where a row asks for nothing, so that what stands in
+// them (padding, NaN) reaches no sum. The plan then sees rows that are scored but have no target of their own (id V of
 // V + 1), and keeps the units that hold a given token.
 cce_status backward_split(const cce_problem* p, const void* E, const void* C, const void* bias, const int64_t* targets,
                           const float* lse, const float* tile_max, const int64_t* count, const float* grad_out,
@@ -360,12 +361,12 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   const int de_split = lp != nullptr && !(filter_eps > 0.f)
                            ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(shares, w.plan.chunk_vt / 4)))
                            : 1;
-  const void* E_in = E;
+  const void* E_dc = E;  // what dC is formed from
   if (lp != nullptr) {
     targets = lw.prep.targets;
     lse = lw.prep.lse;
     grad_out = lw.prep.one;
-    E = lw.prep.E_out;
+    E_dc = lw.prep.E_out;
   }
   {
     cce::PlanArgs PA{};
@@ -414,9 +415,10 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
       P.inv_t = 1.f / lp->temperature;
       P.lse_in = lp->lse;
       P.entropy = lp->entropy;
+      P.logprobs = lp->logprobs;
       P.g_logprobs = lp->g_logprobs;
       P.g_entropy = lp->g_entropy;
-      P.E = static_cast<const __nv_bfloat16*>(E_in);
+      P.E = static_cast<const __nv_bfloat16*>(E);
       P.masked_id = p->ignore_index;
       CCE_TRY(cce::launch_logprob_prep(P, PA, num_sms, s));
     }
@@ -451,10 +453,10 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
       return r == CUDA_SUCCESS ? CCE_OK
                                : fail(CCE_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", static_cast<int>(r));
     };
-    CCE_CHECK(map3(&L.tmE64, E, N));
+    CCE_CHECK(map3(&L.tmE64, E_dc, N));
     CCE_CHECK(map3(&L.tmC64, C, V));
   } else {
-    CCE_CHECK(make_map(&L.tmE64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, E, N, D, 64, 64));
+    CCE_CHECK(make_map(&L.tmE64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, E_dc, N, D, 64, 64));
     CCE_CHECK(make_map(&L.tmC64, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, C, V, D, 64, 64));
   }
   CCE_CHECK(make_map(&L.tmdE, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dE_acc, N, D, 32, 32));
@@ -516,6 +518,7 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
     A.lp_tok_g = lw.prep.tok_g;
     A.lp_k = lp->K;
     A.lp_inv_t = 1.f / lp->temperature;
+    A.lp_scale = lw.prep.row_scale;
   }
   A.err = &w.hdr->err;
   A.timeout_ns = cce::wait_timeout_ns();
@@ -550,6 +553,7 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   F.ls_v = ls_v;
   F.E = Eb;
   F.C = static_cast<const __nv_bfloat16*>(C);
+  F.row_scale = lp != nullptr ? lw.prep.row_scale : nullptr;
   F.csum = smooth ? w.csum : nullptr;
   F.wsum = smooth ? w.wsum : nullptr;
   F.dE_acc = dE_acc;

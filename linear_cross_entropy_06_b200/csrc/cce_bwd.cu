@@ -530,6 +530,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float lp_log2 = (LP && r < A.N) ? A.lp_coef_log[r] * 0.6931471805599453f : 0.f;
         const float lp_scale = LP ? A.lp_inv_t * kLog2e : 0.f;
         const int lp_tok0 = (LP && r < A.N) ? A.lp_tok[r] : -1;
+        const float lp_rscale = (LP && r < A.N) ? A.lp_scale[r] : 0.f;
         const float sc = (r < A.N) ? A.scale[r] : 0.f;
         const float sc_p = sc * fmaf(2.f * A.z_loss, lse_r, 1.f);  // softmax part: (1 + 2 zl LSE) p
         const float sc_y = sc * A.onehot_coef;                     // onehot part: (1 - ls) y
@@ -582,9 +583,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int e = 0; e < 32; ++e) v[e] += e == at ? gk : 0.f;
                   }
                 }
+                // a row that asks for nothing is 0 whatever its logits are (S comes from E as it is)
+                const int left = lse_r != INFINITY ? A.V - col0 : 0;
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                  if (col0 + e >= A.V) v[e] = 0.f;
+                  if (e >= left) v[e] = 0.f;
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = sc_p * exp2f(fmaf(v[e], kLog2e, -lse_l2));
@@ -602,6 +605,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                              pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
               }
               if (A.dbias != nullptr) {  // dbias += column sums of G (this warp's 32 rows), fp32
+                if constexpr (LP) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] *= lp_rscale;
+                }
                 const float cs = warp_column_sums32(v, lane);
                 if (col0 + lane < A.V && cs != 0.f) atomicAdd(A.dbias + col0 + lane, cs);
               }

@@ -737,7 +737,7 @@ constexpr int kPrepThreads = 128;
 
 __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid_constant__ LogprobPrep P,
                                                                     const __grid_constant__ PlanArgs A) {
-  __shared__ int keep;
+  __shared__ float scale_s;
   const int r = blockIdx.x, lane = threadIdx.x & 31;
   if (r >= P.N) {
     dense_plan(A, static_cast<int64_t>(r - P.N) * kPrepThreads + threadIdx.x,
@@ -747,32 +747,58 @@ __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid
   if (threadIdx.x < 32) {
     const float lse = P.lse_in[r];
     const bool fine = lse != -INFINITY;  // a NaN goes on as NaN
-    float sum = 0.f;
+    float sum = 0.f, lp = 0.f;
     bool any = false;
+    int tok = -1;
     if (lane < P.K) {
       const int64_t id = P.tokens[static_cast<int64_t>(r) * P.K + lane];
       any = id != P.ignore_index && id >= 0 && id < P.V;
       sum = any && fine && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + lane] : 0.f;
-      P.tok[static_cast<int64_t>(lane) * P.N + r] = any && fine ? static_cast<int>(id) : -1;
-      P.tok_g[static_cast<int64_t>(lane) * P.N + r] = sum * P.inv_t;
+      tok = any && fine ? static_cast<int>(id) : -1;
+      if (tok >= 0) lp = P.logprobs[static_cast<int64_t>(r) * P.K + lane];
     }
     any = __any_sync(0xffffffffu, any) && fine;
+    const float g = sum * P.inv_t;
     sum = warp_sum(sum);
+    const float h = any && P.g_entropy != nullptr ? P.g_entropy[r] : 0.f;
+    const float coef = any ? -P.inv_t * (h != 0.f ? fmaf(h, P.entropy[r], sum) : sum) : 0.f;
+    const float coef_log = any ? -P.inv_t * h : 0.f;
+    // the token's entry of G, and the scale that makes it a power of two
+    const float size = fabsf(exp2f(lp * kLog2e) * fmaf(coef_log, fmaxf(lp, -140.f), coef) + g);
+    const float entry = __shfl_sync(0xffffffffu, size, 0);
+    const float s = P.K == 1 && entry > 1e-30f && entry < 1e30f
+                        ? __uint_as_float((__float_as_uint(entry) & 0x7fffffu) | 0x3f800000u)
+                        : 1.f;
+    if (lane < P.K) {
+      P.tok[static_cast<int64_t>(lane) * P.N + r] = tok;
+      P.tok_g[static_cast<int64_t>(lane) * P.N + r] = g / s;
+    }
     if (lane == 0) {
-      const float h = any && P.g_entropy != nullptr ? P.g_entropy[r] : 0.f;
-      P.coef[r] = any ? -P.inv_t * (h != 0.f ? fmaf(h, P.entropy[r], sum) : sum) : 0.f;
-      P.coef_log[r] = any ? -P.inv_t * h : 0.f;
+      P.coef[r] = coef / s;
+      P.coef_log[r] = coef_log / s;
+      P.row_scale[r] = s;
+      scale_s = any ? s : 0.f;
       P.lse[r] = any ? lse : INFINITY;
       P.targets[r] = any ? P.V : P.masked_id;
       A.scale[r] = 1.f;
       if (r == 0) *P.one = 1.f;
-      keep = any;
     }
   }
   __syncthreads();
+  const float s = scale_s;
   const uint4* src = reinterpret_cast<const uint4*>(P.E + static_cast<int64_t>(r) * P.D);
   uint4* dst = reinterpret_cast<uint4*>(P.E_out + static_cast<int64_t>(r) * P.D);
-  for (int d = threadIdx.x; d < P.D / 8; d += kPrepThreads) dst[d] = keep ? src[d] : make_uint4(0, 0, 0, 0);
+  for (int d = threadIdx.x; d < P.D / 8; d += kPrepThreads) {
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (s != 0.f) {
+      const uint4 u = src[d];
+      o.x = pack_bf16x2(s * __uint_as_float(u.x << 16), s * __uint_as_float(u.x & 0xffff0000u));
+      o.y = pack_bf16x2(s * __uint_as_float(u.y << 16), s * __uint_as_float(u.y & 0xffff0000u));
+      o.z = pack_bf16x2(s * __uint_as_float(u.z << 16), s * __uint_as_float(u.z & 0xffff0000u));
+      o.w = pack_bf16x2(s * __uint_as_float(u.w << 16), s * __uint_as_float(u.w & 0xffff0000u));
+    }
+    dst[d] = o;
+  }
   if (A.filter_on) return;
   float4* acc = reinterpret_cast<float4*>(A.dE_acc + static_cast<int64_t>(r) * P.D);
   for (int d = threadIdx.x; d < P.D / 4; d += kPrepThreads) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -947,6 +973,11 @@ __global__ void __launch_bounds__(256, 2) bwd_finalize_kernel(const __grid_const
         const float4 a1 = *reinterpret_cast<const float4*>(src + 4);
         float acc[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
         const float sc = F.scale[r];
+        if (F.row_scale != nullptr) {
+          const float s = F.row_scale[r];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] *= s;
+        }
         if (F.csum != nullptr) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) acc[k] = fmaf(-F.ls_v * sc, cs[k], acc[k]);

@@ -22,8 +22,13 @@ using cce::fail;
 
 // Largest width of 8-bit operands: 127 * 127 * D stays below 2^31.
 constexpr int64_t kInt8MaxD = 131072;
-// K-blocks (of 64 values) summed in one accumulator: see the head of cce_head.cu. 512 values.
+// K-blocks (of 64 values) summed in one accumulator, see the head of cce_head.cu. Every part is read once from tensor
+// memory, which the tensor cores feel (2048 x 2048 x 128256: 785 us with parts of 512 values, 763 with 1024, 752 with
+// the whole sum), and its sum drifts with its length: error of the log-probabilities against 64 bits 2.5e-6, 5.2e-6
+// and 1.1e-5, where fp32 sums have 2.9e-6. Narrow operands, whose fp32 sums are closer, get parts of 256.
 constexpr int kChunkBlocks = 8;
+constexpr int kChunkBlocksNarrow = 4;
+constexpr int64_t kNarrow = 2048;  // widths below
 
 bool sizes_ok(int64_t N, int64_t D, int64_t V, bool int8, bool set_error) {
   auto bad = [&](const char* msg) {
@@ -189,7 +194,7 @@ cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, 
   A->V = static_cast<int>(V);
   const int per_block = int8 ? 128 : 64;  // values of a 128-byte K-block
   A->num_kb = static_cast<int>(ceil_div(D, per_block));
-  A->kb_chunk = int8 ? A->num_kb : kChunkBlocks;
+  A->kb_chunk = int8 ? A->num_kb : D < kNarrow ? kChunkBlocksNarrow : kChunkBlocks;
   A->e_rows = static_cast<int>(std::min<int64_t>(cce::kHeadBM, (N + 7) / 8 * 8));
   A->bias = static_cast<const __nv_bfloat16*>(bias);
   A->e_scale = e_scale;
@@ -356,7 +361,8 @@ size_t cce_logprobs_backward_workspace_size(const cce_logprob_problem* p, int32_
 }
 
 cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, const void* C, const void* bias,
-                                 const int64_t* tokens, const float* lse, const float* entropy, const float* tile_max,
+                                 const int64_t* tokens, const float* logprobs, const float* lse, const float* entropy,
+                                 const float* tile_max,
                                  const float* grad_logprobs, const float* grad_entropy, float filter_eps, void* dE,
                                  void* dC, void* dbias, int32_t out_fp32, int64_t* filtered_tiles, void* workspace,
                                  size_t workspace_bytes, cce_stream_t stream) {
@@ -366,7 +372,8 @@ cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, co
   if (p->num_tokens == 0) return fail(CCE_ERR_INVALID_ARG, "without given tokens there is nothing to differentiate");
   const bool has_rows = p->N > 0;
   if (C == nullptr || dC == nullptr || filtered_tiles == nullptr || workspace == nullptr ||
-      (has_rows && (E == nullptr || tokens == nullptr || lse == nullptr || entropy == nullptr || dE == nullptr ||
+      (has_rows && (E == nullptr || tokens == nullptr || logprobs == nullptr || lse == nullptr || entropy == nullptr ||
+                    dE == nullptr ||
                     (filter_eps > 0.f && tile_max == nullptr))))
     return fail(CCE_ERR_INVALID_ARG, "a required pointer is NULL");
   if (!aligned16(E) || !aligned16(C) || !aligned16(bias) || !aligned16(dE) || !aligned16(dC) || !aligned16(dbias) ||
@@ -383,6 +390,7 @@ cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, co
   g.temperature = p->temperature;
   g.lse = lse;
   g.entropy = entropy;
+  g.logprobs = logprobs;
   g.g_logprobs = grad_logprobs;
   g.g_entropy = grad_entropy;
   return cce::logprobs_backward(&q, g, E, C, bias, tile_max, filter_eps, dE, dC, dbias, out_fp32, filtered_tiles,

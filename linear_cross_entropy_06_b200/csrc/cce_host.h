@@ -48,6 +48,7 @@ struct LogprobGrads {
   float temperature;
   const float* lse;           // [N] of the logits over the temperature
   const float* entropy;       // [N]
+  const float* logprobs;      // [N, K]
   const float* g_logprobs;    // [N, K] or null (zeros)
   const float* g_entropy;     // [N] or null
 };

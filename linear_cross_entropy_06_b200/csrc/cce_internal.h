@@ -200,6 +200,7 @@ struct BwdArgs {
   const float* lp_tok_g;  // [lp_k, N]
   int lp_k;
   float lp_inv_t;         // 1 / temperature
+  const float* lp_scale;  // [N]: see LogprobPrep
   int de_split;           // dE items a row block, slice and chunk: each adds its share of the row block's tiles
 };
 
@@ -264,6 +265,7 @@ struct BwdFinalize {
   float ls_v;                 // label_smoothing / vocab_total
   const __nv_bfloat16* E;
   const __nv_bfloat16* C;
+  const float* row_scale;     // [N] factor of dE_acc's rows (log-probabilities), or null
   const float* csum;          // [D] column sums of C (label smoothing) or null
   const float* wsum;          // [D + 1] sum_r scale_r E_r and sum_r scale_r (label smoothing) or null
   float* dE_acc;              // [N, D] fp32
@@ -323,8 +325,15 @@ cudaError_t launch_fill_zero(void* dst, int64_t bytes, cudaStream_t s);
 // y = z / T, lp_k = y_{t_k} - lse, p = softmax(y) and the gradients g_k of lp_k and h of the entropy H:
 //   dz_v = (1 / T) (sum_k g_k [v = t_k] - p_v (sum_k g_k + h H + h ln p_v)).
 // Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and tok_g[k] = g_k / T for the tokens
-// tok[k] (-1: ignored). A row that asks for nothing, or has no finite logit, gets zeros and lse = +inf
-// (p = 0).
+// tok[k] (-1: ignored), all divided by the row's scale s. A row that asks for nothing, or has no finite
+// logit, gets zeros and lse = +inf (G = 0).
+// The scale: G goes through bf16, and with one token a row dE of a row is mostly that token's entry times
+// its row of C, so an error of that one entry is an error of the whole row. With s in [1, 2) the
+// significand of the entry, it becomes a power of two and is kept exactly: dE is multiplied by s at the
+// end, in fp32, and dC is formed from rows s E, whose rounding to bf16 falls on every element for itself
+// (256 x 128 x 4096, against 64 bits: dE 1.64e-3 and dC 2.2e-3 off, 2.6e-3 and 2.5e-3 without; the exact
+// result rounded to bf16 is 1.65e-3 off). With several tokens s is 1: the other entries are rounded all the
+// same, and dC would carry the rows' rounding besides.
 struct LogprobPrep {
   int N, D, V, K;
   const int64_t* tokens;  // [N, K]
@@ -332,6 +341,7 @@ struct LogprobPrep {
   float inv_t;
   const float* lse_in;
   const float* entropy;
+  const float* logprobs;    // [N, K]
   const float* g_logprobs;  // [N, K] or null
   const float* g_entropy;   // [N] or null
   const __nv_bfloat16* E;
@@ -343,7 +353,8 @@ struct LogprobPrep {
   float* tok_g;
   int64_t* targets;         // V for the other rows: scored, their target in no tile of C
   float* one;               // [1] 1.0: the scale of every row's gradient
-  __nv_bfloat16* E_out;     // [N, D]
+  float* row_scale;         // [N]: s
+  __nv_bfloat16* E_out;     // [N, D]: s E, zero where a row asks for nothing
 };
 // With A.filter_on = 0 it lays out the plan of A as well (every tile kept), and no launch_bwd_plan follows.
 cudaError_t launch_logprob_prep(const LogprobPrep& P, const PlanArgs& A, int num_sms, cudaStream_t s);

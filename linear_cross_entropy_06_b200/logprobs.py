@@ -162,8 +162,8 @@ def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor],
     return logprobs, entropy, lse, tile_max, top_lp, top_ids
 
 
-def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
-                          entropy: torch.Tensor, tile_max: Optional[torch.Tensor],
+def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor, logprobs: torch.Tensor,
+                          lse: torch.Tensor, entropy: torch.Tensor, tile_max: Optional[torch.Tensor],
                           grad_logprobs: Optional[torch.Tensor], grad_entropy: Optional[torch.Tensor],
                           filter_eps: float = 0.0, bias: Optional[torch.Tensor] = None, dbias: Optional[bool] = None,
                           temperature: float = 1.0, ignore_index: int = -100, out_fp32: int = ops.OUT_BF16,
@@ -178,8 +178,8 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     V = rows.shape[0]
     _check_scalars(0, V, temperature)
     K = _check_tokens(tokens, N)
-    for name, t, n in (("lse", lse, N), ("entropy", entropy, N), ("grad_logprobs", grad_logprobs, N * K),
-                       ("grad_entropy", grad_entropy, N)):
+    for name, t, n in (("logprobs", logprobs, N * K), ("lse", lse, N), ("entropy", entropy, N),
+                       ("grad_logprobs", grad_logprobs, N * K), ("grad_entropy", grad_entropy, N)):
         if t is not None and (t.dtype != torch.float32 or t.numel() != n):
             _refuse(f"{name} must be float32 with {n} entries, got {t.dtype} {tuple(t.shape)}")
     if filter_eps > 0.0:
@@ -189,10 +189,11 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     mode = int(out_fp32)
     if mode not in (ops.OUT_BF16, ops.OUT_FP32, ops.OUT_DE_FP32):
         _refuse(f"out_fp32 must be 0, 1 or 2, got {out_fp32!r}")
-    dev = _require_cuda(*(t for t in (E, rows, tokens, lse, entropy, tile_max, grad_logprobs, grad_entropy)
+    dev = _require_cuda(*(t for t in (E, rows, tokens, logprobs, lse, entropy, tile_max, grad_logprobs, grad_entropy)
                           if t is not None))
     E, rows, bias = _aligned(E), _aligned(rows), _aligned(_bias_arg(bias, V, dev))
-    tokens, lse, entropy = tokens.contiguous(), lse.contiguous(), entropy.contiguous()
+    tokens, logprobs = tokens.contiguous(), logprobs.contiguous()
+    lse, entropy = lse.contiguous(), entropy.contiguous()
     g_lp = None if grad_logprobs is None else grad_logprobs.contiguous()
     g_h = None if grad_entropy is None else grad_entropy.contiguous()
     tile_max = None if tile_max is None else tile_max.contiguous()
@@ -210,8 +211,8 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     ws = torch.empty(ws_bytes, device=dev, dtype=torch.uint8)
     with _on(dev):
         _check(lib.cce_logprobs_backward(p, E.data_ptr(), rows.data_ptr(), _ptr(bias), tokens.data_ptr(),
-                                         lse.data_ptr(), entropy.data_ptr(), _ptr(tile_max), _ptr(g_lp), _ptr(g_h),
-                                         float(filter_eps), dE.data_ptr(), dC.data_ptr(), _ptr(db), mode,
+                                         logprobs.data_ptr(), lse.data_ptr(), entropy.data_ptr(), _ptr(tile_max),
+                                         _ptr(g_lp), _ptr(g_h), float(filter_eps), dE.data_ptr(), dC.data_ptr(), _ptr(db), mode,
                                          filtered.data_ptr(), ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
@@ -223,7 +224,7 @@ class _LinearLogprobs(torch.autograd.Function):
     def forward(ctx, E, C, bias, tokens, top_k, temperature, ignore_index, filter_eps):
         logprobs, entropy, lse, tile_max, top_lp, top_ids = cce_logprobs(
             E, C, tokens, top_k, bias, temperature, ignore_index, save_max=filter_eps > 0.0)
-        ctx.save_for_backward(E, C, bias, tokens, lse, entropy, tile_max)
+        ctx.save_for_backward(E, C, bias, tokens, logprobs, lse, entropy, tile_max)
         ctx.cfg = (temperature, ignore_index, filter_eps)
         ctx.set_materialize_grads(False)
         if top_k:
@@ -232,11 +233,11 @@ class _LinearLogprobs(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_logprobs, grad_entropy, _lp, _ids):
-        E, C, bias, tokens, lse, entropy, tile_max = ctx.saved_tensors
+        E, C, bias, tokens, logprobs, lse, entropy, tile_max = ctx.saved_tensors
         temperature, ignore_index, filter_eps = ctx.cfg
         want_db = bias is not None and ctx.needs_input_grad[2]
-        out = cce_logprobs_backward(E, C, tokens, lse, entropy, tile_max, grad_logprobs, grad_entropy, filter_eps,
-                                    bias, want_db, temperature, ignore_index)
+        out = cce_logprobs_backward(E, C, tokens, logprobs, lse, entropy, tile_max, grad_logprobs, grad_entropy,
+                                    filter_eps, bias, want_db, temperature, ignore_index)
         dbias = out[3].to(bias.dtype).reshape(bias.shape) if want_db else None
         return out[0], out[1], dbias, None, None, None, None, None
 

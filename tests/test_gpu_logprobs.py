@@ -10,8 +10,9 @@ Tolerances, derived before the first run. u = 2^-24 is half a step of fp32, 2^-8
           summed in blocks of 64, each term a few u: 2 dz / T + 2^-18 (1 + |lp|).
  entropy  dH = -sum_v p_v (ln p_v + H) dy_v, and sum p |ln p + H| <= 2 H: 2 H dz / T + 2^-18 (1 + H).
  grads    G = p (coef + coef_log ln p) + onehot terms, relative error of p 2 dz / T (2^-18 more for its own
-          roundings), one rounding to bf16 (2^-8 |G|), fp32 sums (2^-12 of the sum of magnitudes, with the cut
-          sums of the tensor cores), and for bf16 outputs one more rounding.
+          roundings), one rounding to bf16 (2^-8 |G|), for dC one of the scaled rows of E (2^-8 |G| |E|), fp32 sums
+          (2^-12 of the sum of magnitudes, with the cut sums of the tensor cores), and for bf16 outputs one more
+          rounding.
 """
 import math
 
@@ -213,7 +214,8 @@ def grad_reference(E, C, bias, tok, T, g, h):
     a = G.abs() + eG
     E, C = E.double() * wanted.any(1)[:, None], C.double()
     dE, dC, db = G @ C, G.T @ E, G.sum(0)
-    tol = (eG @ C.abs() + 2.0 ** -12 * (a @ C.abs()), eG.T @ E.abs() + 2.0 ** -12 * (a.T @ E.abs()),
+    # dC's rows of E carry the rows' scales and are rounded to bf16 with them: 2^-8 more
+    tol = (eG @ C.abs() + 2.0 ** -12 * (a @ C.abs()), eG.T @ E.abs() + (2.0 ** -8 + 2.0 ** -12) * (a.T @ E.abs()),
            eG.sum(0) + 2.0 ** -12 * a.sum(0))
     return (dE, dC, db), tol
 
@@ -227,7 +229,7 @@ def test_gradients(device, N, D, V, K, has_bias, T, out_fp32):
     h = torch.randn(N, generator=gen).to(device)
     lp, H, lse, _, _, _ = L.cce_logprobs(E, C, tok, 0, bias, T, check=True)
     for gg, hh in ((g, h), (g, None), (None, h)):
-        out = L.cce_logprobs_backward(E, C, tok, lse, H, None, gg, hh, 0.0, bias, True, T, out_fp32=out_fp32,
+        out = L.cce_logprobs_backward(E, C, tok, lp, lse, H, None, gg, hh, 0.0, bias, True, T, out_fp32=out_fp32,
                                       check=True)
         ref, tol = grad_reference(E, C, bias, tok, T, torch.zeros_like(g) if gg is None else gg,
                                   torch.zeros_like(h) if hh is None else hh)
