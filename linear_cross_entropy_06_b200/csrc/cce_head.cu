@@ -333,7 +333,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  wait_for_previous_grid();  // the 8-bit rows of E or the transposed tokens, when a kernel of this call made them
+  if (A.clear && blockIdx.x == 0 && threadIdx.x == 0) {  // nothing is reported before the waits below
+    *A.err = 0;
+    *A.failed = 0;
+  }
   const WaitCtl wc{abort_flag, A.err, A.timeout_ns};
   const int num_kb = A.num_kb;
   constexpr int KE = I8 ? KB_BYTES : KB_BYTES / 2;  // values of K a block
@@ -342,6 +345,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   else regs_inc<REGS_MANY>();
   if (warp >= 4) {
     // ---------------- epilogue ----------------
+    wait_for_previous_grid();  // the scales of E or the transposed tokens, when a kernel of this call made them
     const int q = warp & 3;             // tensor-memory lanes of this warp
     const int part = (warp - 4) >> 2;   // columns COLS part .. COLS part + COLS - 1 of a tile
     const uint32_t tmine = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(part * COLS);
@@ -495,23 +499,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued[STAGES] = {0, 0, 0, 0};
-      bool ok = true;
+      bool ok = true, first = true;
       const uint32_t e_bytes = static_cast<uint32_t>(A.e_rows) * KB_BYTES;
       for_tiles(A.split, A.V, [&](const HeadTile& t) {
         const int rows_c = tile_rows(t);
         const uint32_t bytes = e_bytes + static_cast<uint32_t>(rows_c) * KB_BYTES;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) return ok = false;
-          const uint32_t dst = smem_u32(base + stage * STAGE_BYTES);
-          mbar_arrive_expect_tx(full_bar(stage), bytes);
-          tma_load_2d(dst, &tmE, full_bar(stage), kb * KE, t.b * BM);
+        auto load_c = [&](int st, int kb) {
+          const uint32_t dst = smem_u32(base + st * STAGE_BYTES) + A_BYTES;
+          mbar_arrive_expect_tx(full_bar(st), bytes);
           if (rows_c == BN) {
-            tma_load_2d(dst + A_BYTES, &tmC, full_bar(stage), kb * KE, t.col);
+            tma_load_2d(dst, &tmC, full_bar(st), kb * KE, t.col);
           } else {
             for (int j = 0; j < rows_c; j += kHeadUnit)
-              tma_load_2d(dst + A_BYTES + static_cast<uint32_t>(j) * KB_BYTES, &tmC64, full_bar(stage), kb * KE,
-                          t.col + j);
+              tma_load_2d(dst + static_cast<uint32_t>(j) * KB_BYTES, &tmC64, full_bar(st), kb * KE, t.col + j);
           }
+        };
+        // The first stages' rows of C are on their way before the kernel that makes the 8-bit rows of E has ended.
+        int ahead = 0;
+        if (first) {
+          ahead = min(STAGES, num_kb);
+          for (int kb = 0; kb < ahead; ++kb) load_c(kb, kb);
+          wait_for_previous_grid();
+          first = false;
+        }
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (kb >= ahead) {
+            if (!mbar_wait(empty_bar(stage), phase ^ 1u, wc)) return ok = false;
+            load_c(stage, kb);
+          }
+          tma_load_2d(smem_u32(base + stage * STAGE_BYTES), &tmE, full_bar(stage), kb * KE, t.b * BM);
           ++issued[stage];
           if (++stage == STAGES) {
             stage = 0;
@@ -1156,6 +1172,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
 __global__ void __launch_bounds__(256) head_tokens_kernel(const int64_t* __restrict__ tokens, int N, int K, int V,
                                                           int64_t ignore_index, int* __restrict__ tok_t) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  let_next_grid_start();
   if (i >= static_cast<int64_t>(N) * K) return;
   const int64_t id = tokens[i];
   tok_t[(i % K) * N + i / K] = id != ignore_index && id >= 0 && id < V ? static_cast<int>(id) : -1;
@@ -1182,6 +1199,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
                                                                       int64_t D, int8_t* __restrict__ q,
                                                                       float* __restrict__ scale) {
   __shared__ float wmax[kQuantThreads / 32];
+  let_next_grid_start();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const __nv_bfloat16* src = x + r * D;
     float m = 0.f;
@@ -1245,12 +1263,8 @@ cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool af
   return launch_one<false, false>(M, A, after_kernel, s);
 }
 
-// Up to this many rows every pick is computed for its row alone: the rows' picks are then nearly all different, and
-// bringing equal ones together costs more (a launch, and a chain of atomics in the one before) than it saves.
-constexpr int kUngroupedRows = 64;
-
 cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s) {
-  P.grouped = P.N > kUngroupedRows ? 1 : 0;
+  P.grouped = picks_grouped(P.N) ? 1 : 0;
   // with few rows each gets more warps, as the machine is not full
   cudaError_t e = P.N < 2 * sms ? launch_after_previous(head_pick_kernel<32>, dim3(P.N), dim3(1024), 0, s, P)
                                 : launch_after_previous(head_pick_kernel<8>, dim3(P.N), dim3(256), 0, s, P);

@@ -84,6 +84,7 @@ struct HeadArgs {
   int out_fp32;
   int* err;
   int* failed;      // set when a bounded wait ran out
+  int clear;        // the first head kernel of a call clears both
   uint64_t timeout_ns;
   int inject_stall;
 };
@@ -148,7 +149,11 @@ struct HeadFinish {
 };
 
 cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool after_kernel, cudaStream_t s);
-// These two follow a kernel of the same call on s.
+// Up to this many rows every pick is computed for its row alone: the rows' picks are then nearly all different, and
+// bringing equal ones together costs more (a launch, and a chain of atomics in the one before) than it saves.
+constexpr int kUngroupedRows = 64;
+inline bool picks_grouped(int64_t rows) { return rows > kUngroupedRows; }
+// These two follow a kernel of the same call on s. With picks_grouped the counters are zero before.
 cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s);
 cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s);
 cudaError_t launch_head_tokens(const int64_t* tokens, int N, int K, int V, int64_t ignore_index, int* tok_t,

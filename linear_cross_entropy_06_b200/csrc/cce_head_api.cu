@@ -259,9 +259,10 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
   CCE_CHECK(cce::get_encoder());
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int K = p->num_tokens, top_k = p->top_k;
-  // one memset clears the header and, directly behind it, the first slab's counters
-  CCE_TRY(cudaMemsetAsync(w.hdr, 0, top_k > 0 ? cce::kHeaderBytes + w.counter_bytes : sizeof(cce::WsHeader), s));
-  if (!has_rows) return CCE_OK;
+  if (!has_rows) {
+    CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(cce::WsHeader), s));
+    return CCE_OK;
+  }
   if (int8)
     CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), p->N, p->D, w.e8, w.e_scale, s));
 
@@ -272,12 +273,14 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     const void* operand = int8 ? static_cast<const void*>(w.e8 + r0 * p->D) : Eb;
     const float* e_scale = int8 ? w.e_scale + r0 : nullptr;
     const int64_t* tok = K > 0 ? tokens + r0 * K : nullptr;
-    if (r0 > 0) CCE_TRY(cudaMemsetAsync(w.counters, 0, w.counter_bytes, s));
+    // the header is cleared by the head kernel
+    if (top_k > 0 && cce::picks_grouped(n)) CCE_TRY(cudaMemsetAsync(w.counters, 0, w.counter_bytes, s));
     if (K > 1) CCE_TRY(cce::launch_head_tokens(tok, static_cast<int>(n), K, static_cast<int>(p->V), p->ignore_index,
                                                w.tok_t, s));
     cce::HeadArgs A{};
     cce::HeadMaps M;
     CCE_CHECK(head_args(n, p->D, p->V, int8, operand, e_scale, C, bias, c_scale, w, sms, &A, &M));
+    A.clear = r0 == 0;
     A.tokens = tok;
     A.tok_t = w.tok_t;
     A.ignore_index = p->ignore_index;
@@ -290,8 +293,9 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     A.part_m = w.part_m;
     A.part_s = w.part_s;
     A.part_w = w.part_w;
-    // it follows a kernel directly where the operands or the tokens were prepared on the stream
-    CCE_TRY(cce::launch_head(M, A, int8, K > 1 || (int8 && r0 == 0), s));
+    // it follows a kernel directly where the tokens, or the operands and no counters, were prepared on the stream
+    const bool cleared = top_k > 0 && cce::picks_grouped(n);
+    CCE_TRY(cce::launch_head(M, A, int8, K > 1 || (int8 && r0 == 0 && !cleared), s));
 
     cce::HeadPicks P{};
     if (top_k > 0) {
@@ -433,12 +437,15 @@ cce_status cce_int8_linear(int64_t N, int64_t D, int64_t V, const void* E, const
   CCE_CHECK(cce::check_device(&sms));
   CCE_CHECK(cce::get_encoder());
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(cce::WsHeader), s));
-  if (N == 0) return CCE_OK;
+  if (N == 0) {
+    CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(cce::WsHeader), s));
+    return CCE_OK;
+  }
   CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), N, D, w.e8, w.e_scale, s));
   cce::HeadArgs A{};
   cce::HeadMaps M;
   CCE_CHECK(head_args(N, D, V, true, w.e8, w.e_scale, C, bias, c_scale, w, sms, &A, &M));
+  A.clear = 1;
   A.inv_t = 1.f;
   A.out = out;
   A.out_fp32 = out_fp32;

@@ -117,45 +117,59 @@ def _check_scalars(top_k: int, V: int, temperature: float) -> None:
         raise ValueError(f"the number of alternatives must be in [0, {min(MAX_TOP, V)}], got {top_k}")
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(dev: torch.device):
     """The device of a call as the current one (entering the context costs more than looking)."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor], top_k: int = 0,
                  bias: Optional[torch.Tensor] = None, temperature: float = 1.0, ignore_index: int = -100,
-                 save_max: bool = False, check: bool = False):
+                 save_max: bool = False, check: bool = False, save_lse: bool = True):
     """Run the forward for E [N, D] and tokens [N, K] (or None). Returns (logprobs [N, K], entropy [N],
     lse [N], tile_max or None, top_logprobs [N, top_k], top_ids [N, top_k]) as device tensors; the first
     three are None without tokens, the last two without alternatives. ``save_max`` keeps what a backward
-    that skips units needs."""
+    that skips units needs; without ``save_lse`` lse is None."""
     lib = ops.load_library()
     N, D = _check_matrix(E)
     rows, scale = _check_classifier(C, D)
     V = rows.shape[0]
     _check_scalars(top_k, V, temperature)
     K = 0 if tokens is None else _check_tokens(tokens, N)
-    dev = _require_cuda(*(t for t in (E, rows, scale, tokens) if t is not None))
-    E, rows, scale, bias = _aligned(E), _aligned(rows), _aligned(scale), _aligned(_bias_arg(bias, V, dev))
-    tokens = None if tokens is None else tokens.contiguous()
+    dev = _require_cuda(E, rows)
+    E, rows = _aligned(E), _aligned(rows)
+    if scale is not None:
+        _require_cuda(E, scale)
+        scale = _aligned(scale)
+    if bias is not None:
+        bias = _aligned(_bias_arg(bias, V, dev))
+    if K:
+        _require_cuda(E, tokens)
+        tokens = tokens.contiguous()
     p = ctypes.byref(ops.LogprobProblem(N, D, V, ignore_index, K, top_k, temperature, scale is not None, 0))
     ws_bytes = lib.cce_logprobs_workspace_size(p)
     if ws_bytes == 0:
         _refuse(f"bad problem N={N} D={D} V={V} tokens={K} top_k={top_k} ignore_index={ignore_index}")
     logprobs = entropy = lse = tile_max = top_lp = top_ids = None
+    lse_bytes = 4 * N if K and not save_lse else 0  # kept behind the workspace then
+    ws = torch.empty(ws_bytes + lse_bytes, device=dev, dtype=torch.uint8)
+    lse_ptr = ws.data_ptr() + ws_bytes
     if K:
         logprobs = torch.empty(N, K, device=dev, dtype=torch.float32)
         entropy = torch.empty(N, device=dev, dtype=torch.float32)
-        lse = torch.empty(N, device=dev, dtype=torch.float32)
+        if save_lse:
+            lse = torch.empty(N, device=dev, dtype=torch.float32)
+            lse_ptr = lse.data_ptr()
     if save_max:
         tile_max = torch.empty(max(-(-V // 64) * N, 1), device=dev, dtype=torch.float32)
     if top_k:
         top_lp = torch.empty(N, top_k, device=dev, dtype=torch.float32)
         top_ids = torch.empty(N, top_k, device=dev, dtype=torch.int64)
-    ws = torch.empty(ws_bytes, device=dev, dtype=torch.uint8)
     with _on(dev):
         _check(lib.cce_logprobs(p, E.data_ptr(), rows.data_ptr(), _ptr(scale), _ptr(bias), _ptr(tokens),
-                                _ptr(logprobs), _ptr(entropy), _ptr(lse), _ptr(tile_max), _ptr(top_lp), _ptr(top_ids),
+                                _ptr(logprobs), _ptr(entropy), lse_ptr, _ptr(tile_max), _ptr(top_lp), _ptr(top_ids),
                                 ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
@@ -275,7 +289,7 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
             raise ValueError("shift needs one token a position and a sequence axis of length >= 1")
         tokens = ops.shift_targets(tokens, ignore_index)
     E = _flat(e)
-    t = tokens.to(torch.int64)
+    t = tokens if tokens.dtype == torch.int64 else tokens.to(torch.int64)
     if not many:
         t = t.reshape(-1, 1)
     elif t.dim() != 2:
@@ -283,14 +297,15 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
     grad = torch.is_grad_enabled() and (e.requires_grad or (bias is not None and bias.requires_grad) or
                                         (isinstance(c, torch.Tensor) and c.requires_grad))
     if not grad:
-        logprobs, entropy, _, _, top_lp, top_ids = cce_logprobs(E, c, t, top_k, bias, temperature, ignore_index)
+        logprobs, entropy, _, _, top_lp, top_ids = cce_logprobs(E, c, t, top_k, bias, temperature, ignore_index,
+                                                                save_lse=False)
     elif isinstance(c, Int8Rows):
         raise ValueError("a classifier of 8-bit integers has no gradient: call under torch.no_grad(), or detach e and "
                          "bias")
     else:
         logprobs, entropy, top_lp, top_ids = _LinearLogprobs.apply(E, c, bias, t, int(top_k), float(temperature),
                                                                    ignore_index, float(filter_eps))
-    logprobs = logprobs.reshape(tokens.shape)
+    logprobs = logprobs.view(tokens.shape)
     if len(lead) != 1:
         entropy = entropy.reshape(lead)
         if top_k:
