@@ -347,7 +347,8 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   float* dE_acc = e32 ? static_cast<float*>(dE) : w.dE_acc;
   float* dbias_acc = dbias == nullptr ? nullptr : (c32 ? static_cast<float*>(dbias) : w.dbias_acc);
 
-  CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(WsHeader), s));
+  // (the kernel that lays out a dense plan clears the header)
+  if (N == 0 || lp == nullptr || filter_eps > 0.f) CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(WsHeader), s));
   if (N == 0) {  // no rows: dC = 0 (and dbias = 0)
     CCE_TRY(cce::launch_fill_zero(dC, V * D * (c32 ? 4 : 2), s));
     if (dbias != nullptr) CCE_TRY(cce::launch_fill_zero(dbias, V * (c32 ? 4 : 2), s));
@@ -356,7 +357,7 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   }
   // A dE item runs through every tile of its row block in a chunk: with fewer of them than SMs (row blocks x slices of
   // D) they are what the others wait for, so each is split over as many as fill the machine, of 8 stages at least.
-  // 513 x 1032 x 32003 (25 items of 502 stages): 354 us without, @@ with.
+  // 513 x 1032 x 32003 (25 items of 502 stages): 354 us without, 210 with.
   const int64_t shares = ceil_div(num_sms, std::max<int64_t>(w.plan.nb * w.plan.S, 1));
   const int de_split = lp != nullptr && !(filter_eps > 0.f)
                            ? static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(shares, w.plan.chunk_vt / 4)))

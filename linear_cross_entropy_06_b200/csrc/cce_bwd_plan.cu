@@ -720,6 +720,7 @@ __device__ void dense_plan(const PlanArgs& A, int64_t gtid, int64_t gthreads) {
     }
     P.grp_start[++g] = at += sums(n - 1);
     P.hp_b[tiles] = nb * T;
+    *A.err = 0;
     *P.nchunks_dev = n;
     *P.n_empty = 0;
     *A.filtered_tiles = 0;

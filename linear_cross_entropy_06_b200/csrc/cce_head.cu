@@ -11,7 +11,8 @@
 // S to S f and W to f (W + S d'), f = 2^d', d' = (m - m') log2(e) / temperature.
 //
 // Design (B200): one persistent block per SM, 20 warps.
-//   warp 0       producer: E and C K-blocks of 128 bytes (128B swizzle) by TMA into a 4-stage ring.
+//   warp 0       producer: E and C K-blocks of 128 bytes (128B swizzle) by TMA into a ring of 4 stages (3 where the
+//                logits go out).
 //   warp 1       tensor memory owner; one lane issues tcgen05.mma, M = 128 rows, N = up to 256 columns.
 //   warps 4..19  epilogue, four warps for each 32 rows (one for each 64 columns of the tile): a thread owns
 //                64 logits of one row, in registers. Four warps a scheduler hide the latency of tensor memory
@@ -35,7 +36,6 @@ namespace {
 constexpr int BM = kHeadBM;
 constexpr int BN = kHeadBN;
 constexpr int KB_BYTES = 128;  // one swizzle row: 64 bf16 or 128 8-bit values of K
-constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * KB_BYTES;
 constexpr int B_BYTES = BN * KB_BYTES;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -43,10 +43,16 @@ constexpr int EPI_WARPS = 16;
 constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int COLS = BN / (EPI_WARPS / 4);  // columns of a thread
 constexpr int TMEM_COLS = 512;
-constexpr int NUM_BARRIERS = 2 * STAGES + 4 + 1;
-constexpr int SCRATCH_WARP = 2048;  // of each epilogue warp: a piece of the logits on its way out
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * SCRATCH_WARP + NUM_BARRIERS * 8 + 16;
-static_assert(SMEM_BYTES <= 232448, "fits the 227 KB opt-in shared memory of an SM");
+// Stages of the ring; where the logits go out, one less, and a piece of shared memory for each epilogue warp to pass
+// them through (32 rows of 128 bytes).
+template <bool OUT>
+struct Layout {
+  static constexpr int kStages = OUT ? 3 : 4;
+  static constexpr int kScratchWarp = OUT ? 4096 : 0;
+  static constexpr int kBarriers = 2 * kStages + 4 + 1;
+  static constexpr int kBytes = 1024 + kStages * STAGE_BYTES + EPI_WARPS * kScratchWarp + kBarriers * 8 + 16;
+  static_assert(kBytes <= 232448, "fits the 227 KB opt-in shared memory of an SM");
+};
 static_assert(COLS == kSubTile && COLS == 4 * kHeadPick, "a thread's columns are one saved maximum, and four picks");
 
 // Registers a thread: 640 threads are launched with 96 each; the first warpgroup hands 32 of its own to the four that
@@ -235,57 +241,65 @@ __device__ __forceinline__ void add_powers(const float (&a)[COLS], float m, floa
   w += x + y;
 }
 
-// Writes a warp's 32 rows x COLS columns of logits. A thread's own 32 bytes of a row at a time where rows start on
-// 32-byte boundaries (whole sectors); else 32 columns at a time through the warp's scratch, so that the warp
-// writes runs of one row.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src),
+               "r"(x), "r"(y)
                : "memory");
 }
 
-__device__ __forceinline__ void write_logits(const HeadArgs& A, const float (&a)[COLS], int row0, int col0, int ncol,
-                                             int lane, uint8_t* scratch) {
-  const int per_sector = A.out_fp32 ? 8 : 16;
-  if (A.V % per_sector == 0 && (reinterpret_cast<uintptr_t>(A.out) & 31u) == 0 && ncol % per_sector == 0) {
-    if (row0 + lane >= A.N) return;
-    const int64_t o = static_cast<int64_t>(row0 + lane) * A.V + col0;
-    if (A.out_fp32) {
+// Writes a warp's 32 rows x COLS columns of logits through its scratch. Where rows start on 16-byte boundaries, as
+// 128-byte rows by TMA, which clips them to the tensor (2048 x 2048 x 128256 in bf16: 506 us; 515 us by 32-byte
+// stores of each thread's own row, which keep the memory pipe busy with four pieces of every line; 401 us without
+// writing anything); else the warp writes runs of 32 columns of one row.
+__device__ __forceinline__ void write_logits(const HeadArgs& A, const CUtensorMap& tmOut, const float (&a)[COLS],
+                                             int row0, int col0, int ncol, int lane, uint8_t* scratch) {
+  const uint32_t buf = smem_u32(scratch);
+  if (A.out_tma) {
+    const uint32_t mine = buf + static_cast<uint32_t>(lane) * 128u;
+    const uint32_t x = static_cast<uint32_t>(lane & 7);
+    for (int h = 0; h < (A.out_fp32 ? 2 : 1); ++h) {  // 64 columns of bf16, or 32 of fp32, a box
+      if (lane == 0) bulk_wait_group_read0();
+      __syncwarp();
+      if (A.out_fp32) {
 #pragma unroll
-      for (int j = 0; j < COLS / 8; ++j) {
-        if (8 * j >= ncol) break;
-        uint32_t u[8];
+        for (int c = 0; c < 8; ++c) {
+          const int i = 4 * c;
+          const float v0 = h == 0 ? a[i] : a[i + 32], v1 = h == 0 ? a[i + 1] : a[i + 33],
+                      v2 = h == 0 ? a[i + 2] : a[i + 34], v3 = h == 0 ? a[i + 3] : a[i + 35];
+          st_shared_v4(mine + ((static_cast<uint32_t>(c) ^ x) << 4), __float_as_uint(v0), __float_as_uint(v1),
+                       __float_as_uint(v2), __float_as_uint(v3));
+        }
+      } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(a[8 * j + i]);
-        store32(static_cast<float*>(A.out) + o + 8 * j, u);
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4(mine + ((static_cast<uint32_t>(c) ^ x) << 4), pack_bf16x2(a[8 * c], a[8 * c + 1]),
+                       pack_bf16x2(a[8 * c + 2], a[8 * c + 3]), pack_bf16x2(a[8 * c + 4], a[8 * c + 5]),
+                       pack_bf16x2(a[8 * c + 6], a[8 * c + 7]));
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < COLS / 16; ++j) {
-        if (16 * j >= ncol) break;
-        uint32_t u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(a[16 * j + 2 * i], a[16 * j + 2 * i + 1]);
-        store32(static_cast<__nv_bfloat16*>(A.out) + o + 16 * j, u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && 32 * h < ncol) {
+        tma_store_2d(&tmOut, buf, col0 + 32 * h, row0);
+        bulk_commit_group();
       }
     }
     return;
   }
   const int n_rows = min(32, A.N - row0);
+  float* st = reinterpret_cast<float*>(scratch);
 #pragma unroll
-  for (int j = 0; j < COLS / 16; ++j) {
-    if (16 * j >= ncol) break;
-    // 32 rows x 16 columns, column c of row k at word 16 k + (c + k / 2) % 16: no bank meets twice on the way in
-    float* st = reinterpret_cast<float*>(scratch);
+  for (int j = 0; j < COLS; j += 32) {
+    if (j >= ncol) break;
+    // 32 rows x 32 columns, column c of row k at word 32 k + (c + k) % 32: no bank meets twice, in or out
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) st[lane * 16 + ((i + (lane >> 1)) & 15)] = a[16 * j + i];
+    for (int i = 0; i < 32; ++i) st[lane * 32 + ((i + lane) & 31)] = a[j + i];
     __syncwarp();
-    const int c = lane & 15;
-    for (int k = lane >> 4; k < n_rows; k += 2) {  // two rows a step
-      const float v = st[k * 16 + ((c + (k >> 1)) & 15)];
-      const int64_t o = static_cast<int64_t>(row0 + k) * A.V + col0 + 16 * j + c;
-      if (16 * j + c < ncol) {
+    const bool in = j + lane < ncol;
+    for (int k = 0; k < n_rows; ++k) {
+      const float v = st[k * 32 + ((lane + k) & 31)];
+      const int64_t o = static_cast<int64_t>(row0 + k) * A.V + col0 + j + lane;
+      if (in) {
         if (A.out_fp32) static_cast<float*>(A.out)[o] = v;
         else static_cast<__nv_bfloat16*>(A.out)[o] = __float2bfloat16_rn(v);
       }
@@ -297,12 +311,14 @@ __device__ __forceinline__ void write_logits(const HeadArgs& A, const float (&a)
 template <bool I8, bool OUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     head_kernel(const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmC,
-                const __grid_constant__ CUtensorMap tmC64, const __grid_constant__ HeadArgs A) {
+                const __grid_constant__ CUtensorMap tmC64, const __grid_constant__ CUtensorMap tmOut,
+                const __grid_constant__ HeadArgs A) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int STAGES = Layout<OUT>::kStages, kScratchWarp = Layout<OUT>::kScratchWarp;
   uint8_t* scratch = base + STAGES * STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + EPI_WARPS * SCRATCH_WARP);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NUM_BARRIERS);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + EPI_WARPS * kScratchWarp);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + Layout<OUT>::kBarriers);
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bar0 = smem_u32(bars);
@@ -433,7 +449,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         if constexpr (OUT) {
-          write_logits(A, a, row0, col0, ncol, lane, scratch + (warp - 4) * SCRATCH_WARP);
+          write_logits(A, tmOut, a, row0, col0, ncol, lane, scratch + (warp - 4) * kScratchWarp);
         } else {
           const bool cut = ncol < COLS;
           if (cut) {
@@ -462,7 +478,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           const float mt = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
           if (r < A.N) {
-            if (A.tile_max != nullptr) A.tile_max[static_cast<int64_t>(col0 / kSubTile) * A.N + r] = mt * A.inv_t;
+            if (A.tile_max != nullptr) A.tile_max[col0 / kSubTile * A.max_pitch + r] = mt * A.inv_t;
             if (A.pick_max != nullptr)
               *reinterpret_cast<float4*>(A.pick_max + static_cast<int64_t>(r) * A.picks + col0 / kHeadPick) =
                   make_float4(cm[0], cm[1], cm[2], cm[3]);
@@ -498,7 +514,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (lane == 0 && !A.inject_stall) {
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t issued[STAGES] = {0, 0, 0, 0};
+      uint32_t issued[STAGES] = {};
       bool ok = true, first = true;
       const uint32_t e_bytes = static_cast<uint32_t>(A.e_rows) * KB_BYTES;
       for_tiles(A.split, A.V, [&](const HeadTile& t) {
@@ -586,6 +602,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   }
 
+  if (OUT && warp >= 4) {  // every store of the logits is complete before the kernel ends
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
+  }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) *A.failed = 1;  // what follows then writes NaN
@@ -878,127 +898,6 @@ __global__ void __launch_bounds__(256) head_scatter_kernel(const __grid_constant
   if (u >= 0) P.rows[P.base[u] + P.slot[p]] = p;
 }
 
-__device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16x8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// A work item: 16 columns x up to 64 gathered rows. The operands are the rows themselves, read 64 bytes a row and
-// step: the WARPS warps take the steps in turn and their sums are added through shared memory. Four warps, and four
-// blocks an SM, where there are many items (2048 rows of D = 2048: 116 us, 120 with eight warps and two blocks),
-// eight where there are few and each should be done soon. A lane's 16 bytes
-// of a row feed two instructions whose K positions are the same bytes of both operands, so nothing is rearranged.
-// Rows picked by index suit neither a TMA box nor an M = 128 tile (a pick has 7 rows of 2048 on average); the warp
-// instruction's 16-row tile wastes little, and the kernel is bound by reading C once.
-constexpr int kDotStep = 64;  // bytes of a row a step
-// Steps of a warp summed in one accumulator: 512 values (see the head of the file).
-constexpr int kDotPart = 512 * 2 / kDotStep;
-
-template <bool I8, int WARPS, int TILES, int UNROLL, typename Acc>
-__device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, const int* ids,
-                                         Acc* red, int64_t pitch, int lane, int w) {
-  const int g = lane >> 2, t = lane & 3;
-  const int steps = static_cast<int>((pitch + kDotStep - 1) / kDotStep);
-  const char* er[TILES][2];
-#pragma unroll
-  for (int mt = 0; mt < TILES; ++mt)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      er[mt][h] = static_cast<const char*>(P.E) + (ids[min(16 * mt + 8 * h + g, n - 1)] >> 5) * pitch + t * 16;
-  const char* cr[2];
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
-    cr[nt] = static_cast<const char*>(P.C) + min(pick * kHeadPick + 8 * nt + g, P.V - 1) * pitch + t * 16;
-  Acc sum[TILES][2][4] = {};
-  for (int s0 = 0; s0 < steps; s0 += kDotPart * WARPS) {
-    Acc acc[TILES][2][4] = {};
-    const int s1 = min(steps, s0 + kDotPart * WARPS);
-    for (int s = s0 + w; s < s1; s += WARPS * UNROLL) {
-      uint4 b[UNROLL][2], a[UNROLL][TILES][2];
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int64_t off = static_cast<int64_t>(s + u * WARPS) * kDotStep;
-        const bool in = s + u * WARPS < s1 && off + t * 16 < pitch;
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) b[u][nt] = in ? ld_global_nc_v4(cr[nt] + off) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int mt = 0; mt < TILES; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            a[u][mt][h] = in ? ld_global_nc_v4(er[mt][h] + off) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-        for (int mt = 0; mt < TILES; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const uint4 x = a[u][mt][0], y = a[u][mt][1];
-            mma_16x8(acc[mt][nt], x.x, y.x, x.y, y.y, b[u][nt].x, b[u][nt].y);
-            mma_16x8(acc[mt][nt], x.z, y.z, x.w, y.w, b[u][nt].z, b[u][nt].w);
-          }
-    }
-#pragma unroll
-    for (int mt = 0; mt < TILES; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[mt][nt][i] += acc[mt][nt][i];
-  }
-#pragma unroll
-  for (int mt = 0; mt < TILES; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[(16 * mt + g + 8 * (i >> 1)) * kHeadPick + 8 * nt + 2 * t + (i & 1)] = sum[mt][nt][i];
-}
-
-template <bool I8, int WARPS, int ROWS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) head_dots_kernel(const __grid_constant__ HeadPicks P) {
-  using Acc = typename std::conditional<I8, int, float>::type;
-  __shared__ Acc red[WARPS][ROWS * kHeadPick];
-  __shared__ int ids[kHeadDotRows];
-  wait_for_previous_grid();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t pitch = static_cast<int64_t>(P.D) * (I8 ? 1 : 2);  // a multiple of 16 bytes
-  const int nitems = P.grouped ? P.done[1] : P.N * 32;
-  for (int it = blockIdx.x; it < nitems; it += gridDim.x) {
-    const int3 item = P.grouped ? P.items[it] : make_int3(P.pick[it], it, 1);
-    if (item.x < 0) continue;
-    __syncthreads();  // the previous item's sums and ids have been read
-    if (threadIdx.x < item.z) ids[threadIdx.x] = P.grouped ? P.rows[item.y + threadIdx.x] : it;
-    __syncthreads();
-    if (ROWS <= 16 || item.z <= 16) dot_item<I8, WARPS, 1, 4>(P, item.x, item.z, ids, red[w], pitch, lane, w);
-    else dot_item<I8, WARPS, ROWS / 16, 1>(P, item.x, item.z, ids, red[w], pitch, lane, w);
-    __syncthreads();
-    for (int i = threadIdx.x; i < item.z * kHeadPick; i += WARPS * 32) {
-      Acc z = 0;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) z += red[k][i];
-      const int p = ids[i / kHeadPick], col = item.x * kHeadPick + i % kHeadPick;
-      if (col < P.V) {
-        float v = static_cast<float>(z);
-        if (I8) v *= P.e_scale[p >> 5] * P.c_scale[col];
-        if (P.bias != nullptr) v += __bfloat162float(P.bias[col]);
-        P.logits[static_cast<int64_t>(p) * kHeadPick + i % kHeadPick] = v;
-      }
-    }
-  }
-}
-
 // The row's softmax statistics from those of its segments: (m, s, w) and (m2, s2, w2) -> (m, s, w) of both.
 __device__ __forceinline__ void join_stats(float& m, float& s, float& w, float m2, float s2, float w2, float sc) {
   const float mn = fmaxf(m, m2);
@@ -1026,9 +925,9 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
   __shared__ double exact[32];
   __shared__ unsigned run_mask;
   wait_for_previous_grid();
-  const int lane = threadIdx.x & 31, wi = (threadIdx.x >> 5) % WARPS;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x >> 5) / WARPS;
   if (r >= F.N) return;  // ROWS > 1 only: there nothing below waits for other warps
+  const int lane = threadIdx.x & 31, wi = (threadIdx.x >> 5) % WARPS;
   const HeadSplit& S = F.split;
   const int b = static_cast<int>(r / kHeadBM);
   int g = static_cast<int>(static_cast<long long>(b) * S.ngroups / S.nb);  // the group of row block b, or one off
@@ -1167,6 +1066,132 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
   }
 }
 
+__device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16x8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A work item: 16 columns x up to 64 gathered rows. The operands are the rows themselves, read 64 bytes a row and
+// step: the WARPS warps take the steps in turn and their sums are added through shared memory. Four warps, and four
+// blocks an SM, where there are many items (2048 rows of D = 2048: 116 us, 120 with eight warps and two blocks),
+// eight where there are few and each should be done soon. A lane's 16 bytes
+// of a row feed two instructions whose K positions are the same bytes of both operands, so nothing is rearranged.
+// Rows picked by index suit neither a TMA box nor an M = 128 tile (a pick has 7 rows of 2048 on average); the warp
+// instruction's 16-row tile wastes little, and the kernel is bound by reading C once.
+constexpr int kDotStep = 64;  // bytes of a row a step
+// Steps of a warp summed in one accumulator: 512 values (see the head of the file).
+constexpr int kDotPart = 512 * 2 / kDotStep;
+
+template <bool I8, int WARPS, int TILES, int UNROLL, typename Acc>
+__device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, const int* ids,
+                                         Acc* red, int64_t pitch, int lane, int w) {
+  const int g = lane >> 2, t = lane & 3;
+  const int steps = static_cast<int>((pitch + kDotStep - 1) / kDotStep);
+  const char* er[TILES][2];
+#pragma unroll
+  for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      er[mt][h] = static_cast<const char*>(P.E) + (ids[min(16 * mt + 8 * h + g, n - 1)] >> 5) * pitch + t * 16;
+  const char* cr[2];
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+    cr[nt] = static_cast<const char*>(P.C) + min(pick * kHeadPick + 8 * nt + g, P.V - 1) * pitch + t * 16;
+  Acc sum[TILES][2][4] = {};
+  for (int s0 = 0; s0 < steps; s0 += kDotPart * WARPS) {
+    Acc acc[TILES][2][4] = {};
+    const int s1 = min(steps, s0 + kDotPart * WARPS);
+    for (int s = s0 + w; s < s1; s += WARPS * UNROLL) {
+      uint4 b[UNROLL][2], a[UNROLL][TILES][2];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int64_t off = static_cast<int64_t>(s + u * WARPS) * kDotStep;
+        const bool in = s + u * WARPS < s1 && off + t * 16 < pitch;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) b[u][nt] = in ? ld_global_nc_v4(cr[nt] + off) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            a[u][mt][h] = in ? ld_global_nc_v4(er[mt][h] + off) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+        for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const uint4 x = a[u][mt][0], y = a[u][mt][1];
+            mma_16x8(acc[mt][nt], x.x, y.x, x.y, y.y, b[u][nt].x, b[u][nt].y);
+            mma_16x8(acc[mt][nt], x.z, y.z, x.w, y.w, b[u][nt].z, b[u][nt].w);
+          }
+    }
+#pragma unroll
+    for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[mt][nt][i] += acc[mt][nt][i];
+  }
+#pragma unroll
+  for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[(16 * mt + g + 8 * (i >> 1)) * kHeadPick + 8 * nt + 2 * t + (i & 1)] = sum[mt][nt][i];
+}
+
+// Ungrouped (ROWS = 16) every row has its own items.
+template <bool I8, int WARPS, int ROWS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+    head_dots_kernel(const __grid_constant__ HeadPicks P) {
+  constexpr bool kGrouped = ROWS > 16;
+  using Acc = typename std::conditional<I8, int, float>::type;
+  __shared__ Acc red[WARPS][ROWS * kHeadPick];
+  __shared__ int ids[kHeadDotRows];
+  wait_for_previous_grid();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int64_t pitch = static_cast<int64_t>(P.D) * (I8 ? 1 : 2);  // a multiple of 16 bytes
+  const int nitems = kGrouped ? P.done[1] : P.N * P.wanted;
+  for (int it = blockIdx.x; it < nitems; it += gridDim.x) {
+    const int pair = it / P.wanted * 32 + it % P.wanted;  // ungrouped: the row's pick
+    const int3 item = kGrouped ? P.items[it] : make_int3(P.pick[pair], 0, 1);
+    __syncthreads();  // the previous item's sums and ids have been read
+    if (threadIdx.x < item.z) ids[threadIdx.x] = kGrouped ? P.rows[item.y + threadIdx.x] : pair;
+    __syncthreads();
+    if (kGrouped || item.x >= 0) {
+      if (ROWS <= 16 || item.z <= 16) dot_item<I8, WARPS, 1, 4>(P, item.x, item.z, ids, red[w], pitch, lane, w);
+      else dot_item<I8, WARPS, ROWS / 16, 1>(P, item.x, item.z, ids, red[w], pitch, lane, w);
+      __syncthreads();
+      for (int i = threadIdx.x; i < item.z * kHeadPick; i += WARPS * 32) {
+        Acc z = 0;
+  #pragma unroll
+        for (int k = 0; k < WARPS; ++k) z += red[k][i];
+        const int p = ids[i / kHeadPick], col = item.x * kHeadPick + i % kHeadPick;
+        if (col < P.V) {
+          float v = static_cast<float>(z);
+          if (I8) v *= P.e_scale[p >> 5] * P.c_scale[col];
+          if (P.bias != nullptr) v += __bfloat162float(P.bias[col]);
+          P.logits[static_cast<int64_t>(p) * kHeadPick + i % kHeadPick] = v;
+        }
+      }
+    }
+  }
+}
+
 // tokens [N, K] -> tok_t [K, N], -1 for those that ask for nothing: the head kernel's warps read a token of 32 rows
 // at once.
 __global__ void __launch_bounds__(256) head_tokens_kernel(const int64_t* __restrict__ tokens, int N, int K, int V,
@@ -1243,13 +1268,13 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
 template <bool I8, bool OUT>
 cudaError_t launch_one(const HeadMaps& M, const HeadArgs& A, bool after_kernel, cudaStream_t s) {
   auto kernel = head_kernel<I8, OUT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<OUT>::kBytes);
   if (e != cudaSuccess) return e;
   if (after_kernel) {
-    e = launch_after_previous(kernel, dim3(A.split.grid), dim3(NUM_THREADS), SMEM_BYTES, s, M.E, M.C, M.C64, A);
+    e = launch_after_previous(kernel, dim3(A.split.grid), dim3(NUM_THREADS), Layout<OUT>::kBytes, s, M.E, M.C, M.C64, M.out, A);
     if (e != cudaSuccess) return e;
   } else {
-    kernel<<<A.split.grid, NUM_THREADS, SMEM_BYTES, s>>>(M.E, M.C, M.C64, A);
+    kernel<<<A.split.grid, NUM_THREADS, Layout<OUT>::kBytes, s>>>(M.E, M.C, M.C64, M.out, A);
   }
   note_launches(1);
   return cudaGetLastError();
@@ -1263,32 +1288,35 @@ cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool af
   return launch_one<false, false>(M, A, after_kernel, s);
 }
 
-cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s) {
+cudaError_t launch_head_picks(HeadPicks P, const HeadFinish& F, bool int8, int sms, cudaStream_t s) {
   P.grouped = picks_grouped(P.N) ? 1 : 0;
   // with few rows each gets more warps, as the machine is not full
   cudaError_t e = P.N < 2 * sms ? launch_after_previous(head_pick_kernel<32>, dim3(P.N), dim3(1024), 0, s, P)
                                 : launch_after_previous(head_pick_kernel<8>, dim3(P.N), dim3(256), 0, s, P);
   if (e != cudaSuccess) return e;
-  if (P.grouped) {
-    e = launch_after_previous(head_scatter_kernel, dim3((P.N * 32 + 255) / 256), dim3(256), 0, s, P);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(std::min(P.N * 32, 4 * sms));
-    e = int8 ? launch_after_previous(head_dots_kernel<true, 4, kHeadDotRows>, grid, dim3(128), 0, s, P)
-             : launch_after_previous(head_dots_kernel<false, 4, kHeadDotRows>, grid, dim3(128), 0, s, P);
-  } else {
-    const dim3 grid(std::min(P.N * 32, 2 * sms));
+  if (!P.grouped) {
+    const dim3 grid(std::min(P.N * P.wanted, 2 * sms));
     e = int8 ? launch_after_previous(head_dots_kernel<true, 8, 16>, grid, dim3(256), 0, s, P)
              : launch_after_previous(head_dots_kernel<false, 8, 16>, grid, dim3(256), 0, s, P);
+    if (e != cudaSuccess) return e;
+    note_launches(2);
+    return launch_head_finish(F, s);
   }
-  note_launches(P.grouped ? 3 : 2);
-  return e;
+  e = launch_after_previous(head_scatter_kernel, dim3((P.N * 32 + 255) / 256), dim3(256), 0, s, P);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(std::min(P.N * 32, 4 * sms));
+  e = int8 ? launch_after_previous(head_dots_kernel<true, 4, kHeadDotRows>, grid, dim3(128), 0, s, P)
+           : launch_after_previous(head_dots_kernel<false, 4, kHeadDotRows>, grid, dim3(128), 0, s, P);
+  if (e != cudaSuccess) return e;
+  note_launches(3);
+  return launch_head_finish(F, s);
 }
 
 cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s) {
-  // A block of eight warps per row where a row has many segments (few row blocks share the machine), so that they are
-  // read at once; else two where alternatives are to be ordered; else a warp per row, four rows a block.
+  // A block of eight warps per row where a row has very many segments (one or two row blocks share the machine), so
+  // that they are read at once; else two where alternatives are to be ordered; else a warp per row, four rows a block.
   cudaError_t e;
-  if (F.split.max_segments() > 16) {
+  if (F.split.max_segments() > 64) {
     e = launch_after_previous(head_finish_kernel<8, 1>, dim3(F.N), dim3(256), 0, s, F);
   } else if (F.top_k > 0) {
     e = launch_after_previous(head_finish_kernel<2, 1>, dim3(F.N), dim3(64), 0, s, F);

@@ -73,7 +73,8 @@ struct HeadArgs {
   int64_t ignore_index;
   int K;
   float* zt;        // [K, N]: logits of the given tokens
-  float* tile_max;  // [ceil(V / 64), N]: largest y of each 64 columns, or null
+  float* tile_max;  // [ceil(V / 64), max_pitch]: largest y of each 64 columns, or null
+  int64_t max_pitch;
   float* pick_max;  // [N, picks]: largest logit of each pick, or null
   int picks;        // a multiple of 4, at least the number of picks
   float inv_t;      // 1 / temperature
@@ -82,6 +83,7 @@ struct HeadArgs {
   float* part_w;
   void* out;        // [N, V] logits (8-bit product)
   int out_fp32;
+  int out_tma;      // rows of out start on 16-byte boundaries
   int* err;
   int* failed;      // set when a bounded wait ran out
   int clear;        // the first head kernel of a call clears both
@@ -115,6 +117,7 @@ struct HeadMaps {
   CUtensorMap E;    // box of e_rows rows x 128 bytes
   CUtensorMap C;    // box of 256 rows
   CUtensorMap C64;  // box of 64 rows
+  CUtensorMap out;  // logits, box of 32 rows x 128 bytes (HeadArgs.out_tma)
 };
 
 struct HeadFinish {
@@ -154,7 +157,8 @@ cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool af
 constexpr int kUngroupedRows = 64;
 inline bool picks_grouped(int64_t rows) { return rows > kUngroupedRows; }
 // These two follow a kernel of the same call on s. With picks_grouped the counters are zero before.
-cudaError_t launch_head_picks(HeadPicks P, bool int8, int sms, cudaStream_t s);
+// The first also launches the finish.
+cudaError_t launch_head_picks(HeadPicks P, const HeadFinish& F, bool int8, int sms, cudaStream_t s);
 cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s);
 cudaError_t launch_head_tokens(const int64_t* tokens, int N, int K, int V, int64_t ignore_index, int* tok_t,
                                cudaStream_t s);

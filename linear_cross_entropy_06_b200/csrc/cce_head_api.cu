@@ -278,7 +278,7 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     if (K > 1) CCE_TRY(cce::launch_head_tokens(tok, static_cast<int>(n), K, static_cast<int>(p->V), p->ignore_index,
                                                w.tok_t, s));
     cce::HeadArgs A{};
-    cce::HeadMaps M;
+    cce::HeadMaps M{};
     CCE_CHECK(head_args(n, p->D, p->V, int8, operand, e_scale, C, bias, c_scale, w, sms, &A, &M));
     A.clear = r0 == 0;
     A.tokens = tok;
@@ -286,7 +286,8 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     A.ignore_index = p->ignore_index;
     A.K = K;
     A.zt = w.zt;
-    A.tile_max = tile_max;
+    A.tile_max = tile_max == nullptr ? nullptr : tile_max + r0;
+    A.max_pitch = p->N;
     A.pick_max = top_k > 0 ? w.pick_max : nullptr;
     A.picks = top_k > 0 ? picks_pitch(p->V) : 0;
     A.inv_t = 1.f / p->temperature;
@@ -297,29 +298,6 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     const bool cleared = top_k > 0 && cce::picks_grouped(n);
     CCE_TRY(cce::launch_head(M, A, int8, K > 1 || (int8 && r0 == 0 && !cleared), s));
 
-    cce::HeadPicks P{};
-    if (top_k > 0) {
-      P.N = A.N;
-      P.D = A.D;
-      P.V = A.V;
-      P.E = operand;
-      P.C = C;
-      P.e_scale = e_scale;
-      P.c_scale = c_scale;
-      P.bias = A.bias;
-      P.pick_max = w.pick_max;
-      P.picks = A.picks;
-      P.wanted = picks_wanted(top_k);
-      P.done = w.counters;
-      P.count = w.counters + 4;
-      P.base = w.base;
-      P.pick = w.pick;
-      P.slot = w.slot;
-      P.rows = w.rows;
-      P.items = w.items;
-      P.logits = w.logits;
-      CCE_TRY(cce::launch_head_picks(P, int8, sms, s));
-    }
     cce::HeadFinish F{};
     F.split = A.split;
     F.N = A.N;
@@ -342,7 +320,7 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     F.part_w = w.part_w;
     F.pick = w.pick;
     F.logits = w.logits;
-    F.wanted = P.wanted;
+    F.wanted = picks_wanted(top_k);
     F.top_k = top_k;
     F.logprobs = K > 0 ? logprobs + r0 * K : nullptr;
     F.entropy = K > 0 ? entropy + r0 : nullptr;
@@ -351,7 +329,31 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     F.top_ids = top_k > 0 ? top_ids + r0 * top_k : nullptr;
     F.err = A.err;
     F.failed = A.failed;
-    CCE_TRY(cce::launch_head_finish(F, s));
+    if (top_k == 0) {
+      CCE_TRY(cce::launch_head_finish(F, s));
+      continue;
+    }
+    cce::HeadPicks P{};
+    P.N = A.N;
+    P.D = A.D;
+    P.V = A.V;
+    P.E = operand;
+    P.C = C;
+    P.e_scale = e_scale;
+    P.c_scale = c_scale;
+    P.bias = A.bias;
+    P.pick_max = w.pick_max;
+    P.picks = A.picks;
+    P.wanted = picks_wanted(top_k);
+    P.done = w.counters;
+    P.count = w.counters + 4;
+    P.base = w.base;
+    P.pick = w.pick;
+    P.slot = w.slot;
+    P.rows = w.rows;
+    P.items = w.items;
+    P.logits = w.logits;
+    CCE_TRY(cce::launch_head_picks(P, F, int8, sms, s));
   }
   return CCE_OK;
 }
@@ -443,12 +445,17 @@ cce_status cce_int8_linear(int64_t N, int64_t D, int64_t V, const void* E, const
   }
   CCE_TRY(cce::launch_quantize_rows(static_cast<const __nv_bfloat16*>(E), N, D, w.e8, w.e_scale, s));
   cce::HeadArgs A{};
-  cce::HeadMaps M;
+  cce::HeadMaps M{};
   CCE_CHECK(head_args(N, D, V, true, w.e8, w.e_scale, C, bias, c_scale, w, sms, &A, &M));
   A.clear = 1;
   A.inv_t = 1.f;
   A.out = out;
   A.out_fp32 = out_fp32;
+  const int64_t out_size = out_fp32 ? 4 : 2;
+  A.out_tma = V * out_size % 16 == 0;
+  if (A.out_tma)
+    CCE_CHECK(cce::make_map(&M.out, out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                            static_cast<size_t>(out_size), out, N, V, static_cast<uint32_t>(128 / out_size), 32));
   CCE_TRY(cce::launch_head(M, A, true, true, s));
   return CCE_OK;
 }

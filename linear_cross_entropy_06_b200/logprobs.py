@@ -22,9 +22,10 @@ import math
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
-from .ops import _bias_arg, _check, _ptr, _require_cuda, _stream
+from .ops import _bias_arg, _check, _ptr, _require_cuda
 
 MAX_TOKENS = 32  # given tokens a position
 MAX_TOP = 24     # alternatives a position
@@ -118,6 +119,11 @@ def _check_scalars(top_k: int, V: int, temperature: float) -> None:
 
 
 _HERE = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone, without a Stream object
+
+
+def _stream(dev: torch.device) -> int:
+    return ops._stream(dev) if _raw_stream is None else _raw_stream(dev.index)
 
 
 def _on(dev: torch.device):
@@ -235,9 +241,10 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
 
 class _LinearLogprobs(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, E, C, bias, tokens, top_k, temperature, ignore_index, filter_eps):
+    def forward(ctx, E, C, bias, tokens, shape, top_k, temperature, ignore_index, filter_eps):
         logprobs, entropy, lse, tile_max, top_lp, top_ids = cce_logprobs(
             E, C, tokens, top_k, bias, temperature, ignore_index, save_max=filter_eps > 0.0)
+        logprobs = logprobs.view(shape)  # here, where it adds no node to the graph
         ctx.save_for_backward(E, C, bias, tokens, logprobs, lse, entropy, tile_max)
         ctx.cfg = (temperature, ignore_index, filter_eps)
         ctx.set_materialize_grads(False)
@@ -246,6 +253,7 @@ class _LinearLogprobs(torch.autograd.Function):
         return logprobs, entropy, top_lp, top_ids
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_logprobs, grad_entropy, _lp, _ids):
         E, C, bias, tokens, logprobs, lse, entropy, tile_max = ctx.saved_tensors
         temperature, ignore_index, filter_eps = ctx.cfg
@@ -253,7 +261,7 @@ class _LinearLogprobs(torch.autograd.Function):
         out = cce_logprobs_backward(E, C, tokens, logprobs, lse, entropy, tile_max, grad_logprobs, grad_entropy,
                                     filter_eps, bias, want_db, temperature, ignore_index)
         dbias = out[3].to(bias.dtype).reshape(bias.shape) if want_db else None
-        return out[0], out[1], dbias, None, None, None, None, None
+        return out[0], out[1], dbias, None, None, None, None, None, None
 
 
 def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -299,13 +307,13 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
     if not grad:
         logprobs, entropy, _, _, top_lp, top_ids = cce_logprobs(E, c, t, top_k, bias, temperature, ignore_index,
                                                                 save_lse=False)
+        logprobs = logprobs.view(tokens.shape)
     elif isinstance(c, Int8Rows):
         raise ValueError("a classifier of 8-bit integers has no gradient: call under torch.no_grad(), or detach e and "
                          "bias")
     else:
-        logprobs, entropy, top_lp, top_ids = _LinearLogprobs.apply(E, c, bias, t, int(top_k), float(temperature),
-                                                                   ignore_index, float(filter_eps))
-    logprobs = logprobs.view(tokens.shape)
+        logprobs, entropy, top_lp, top_ids = _LinearLogprobs.apply(
+            E, c, bias, t, tokens.shape, int(top_k), float(temperature), ignore_index, float(filter_eps))
     if len(lead) != 1:
         entropy = entropy.reshape(lead)
         if top_k:

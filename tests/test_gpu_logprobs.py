@@ -119,6 +119,19 @@ def check_top(E, C, bias, k, T, top, z=None, dz=None):
     assert (err <= 2 * dz[:, None] / T + 2.0 ** -18 * (1 + ref.abs())).all(), err.max().item()
 
 
+def test_saved_maxima_of_a_long_batch_with_alternatives(device):
+    """Alternatives are found a slab of rows at a time; the maxima saved for the backward are those of all rows."""
+    E, C, _, tok = make(4224, 64, 700, 23, device, K=1)
+    lp, H, lse, tmax, tl, ti = L.cce_logprobs(E, C, tok, 3, save_max=True, check=True)
+    plain = L.cce_logprobs(E, C, tok, save_max=True)
+    assert torch.equal(tmax, plain[3])  # (the statistics are added in another order)
+    check_logprobs(E, C, None, tok, 1.0, lp, H)
+    z = torch.full((4224, 704), -math.inf, dtype=torch.float64, device=device)
+    z[:, :700] = logits64(E, C, None)
+    most = z.reshape(4224, 11, 64).amax(2).T
+    assert ((tmax.reshape(11, 4224).double() - most).abs() <= logit_tol(E, C)).all()
+
+
 def test_equal_alternatives_go_to_the_lowest_id(device):
     """Rows of C repeated all over the vocabulary, across tiles and segments; a row of E that is zero (every logit
     equal); logits that differ by less than fp32 can tell."""
