@@ -11,8 +11,7 @@
 // S to S f and W to f (W + S d'), f = 2^d', d' = (m - m') log2(e) / temperature.
 //
 // Design (B200): one persistent block per SM, 20 warps.
-//   warp 0       producer: E and C K-blocks of 128 bytes (128B swizzle) by TMA into a ring of 4 stages (3 where the
-//                logits go out).
+//   warp 0       producer: E and C K-blocks of 128 bytes (128B swizzle) by TMA into a 4-stage ring.
 //   warp 1       tensor memory owner; one lane issues tcgen05.mma, M = 128 rows, N = up to 256 columns.
 //   warps 4..19  epilogue, four warps for each 32 rows (one for each 64 columns of the tile): a thread owns
 //                64 logits of one row, in registers. Four warps a scheduler hide the latency of tensor memory
@@ -35,6 +34,7 @@ namespace {
 
 constexpr int BM = kHeadBM;
 constexpr int BN = kHeadBN;
+constexpr int STAGES = 4;
 constexpr int KB_BYTES = 128;  // one swizzle row: 64 bf16 or 128 8-bit values of K
 constexpr int A_BYTES = BM * KB_BYTES;
 constexpr int B_BYTES = BN * KB_BYTES;
@@ -43,16 +43,10 @@ constexpr int EPI_WARPS = 16;
 constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int COLS = BN / (EPI_WARPS / 4);  // columns of a thread
 constexpr int TMEM_COLS = 512;
-// Stages of the ring; where the logits go out, one less, and a piece of shared memory for each epilogue warp to pass
-// them through (32 rows of 128 bytes).
-template <bool OUT>
-struct Layout {
-  static constexpr int kStages = OUT ? 3 : 4;
-  static constexpr int kScratchWarp = OUT ? 4096 : 0;
-  static constexpr int kBarriers = 2 * kStages + 4 + 1;
-  static constexpr int kBytes = 1024 + kStages * STAGE_BYTES + EPI_WARPS * kScratchWarp + kBarriers * 8 + 16;
-  static_assert(kBytes <= 232448, "fits the 227 KB opt-in shared memory of an SM");
-};
+constexpr int NUM_BARRIERS = 2 * STAGES + 4 + 1;
+constexpr int SCRATCH_WARP = 2048;  // of each epilogue warp: a piece of the logits on its way out (16 rows of 128 bytes)
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * SCRATCH_WARP + NUM_BARRIERS * 8 + 16;
+static_assert(SMEM_BYTES <= 232448, "fits the 227 KB opt-in shared memory of an SM");
 static_assert(COLS == kSubTile && COLS == 4 * kHeadPick, "a thread's columns are one saved maximum, and four picks");
 
 // Registers a thread: 640 threads are launched with 96 each; the first warpgroup hands 32 of its own to the four that
@@ -247,78 +241,102 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 
-// Writes a warp's 32 rows x COLS columns of logits through its scratch. Where rows start on 16-byte boundaries, as
-// 128-byte rows by TMA, which clips them to the tensor (2048 x 2048 x 128256 in bf16: 506 us; 515 us by 32-byte
-// stores of each thread's own row, which keep the memory pipe busy with four pieces of every line; 401 us without
-// writing anything); else the warp writes runs of 32 columns of one row.
+// Writes a warp's 32 rows x COLS columns of logits through its scratch. Where rows start on 16-byte boundaries, by
+// TMA, 16 rows of 128 bytes at a time, which clips them to the tensor; else the warp writes 32 words of a row at a
+// time (1000 x 1024 x 50257: 154 us, 178 by single elements of two rows).
+// 2048 x 2048 x 128256 in bf16: 460 us; 510 by 32-byte stores of each thread's own row, or with 32 rows at a time and
+// one stage of the ring less to make room for them; 401 without writing anything.
+template <bool F32>
 __device__ __forceinline__ void write_logits(const HeadArgs& A, const CUtensorMap& tmOut, const float (&a)[COLS],
                                              int row0, int col0, int ncol, int lane, uint8_t* scratch) {
   const uint32_t buf = smem_u32(scratch);
   if (A.out_tma) {
-    const uint32_t mine = buf + static_cast<uint32_t>(lane) * 128u;
+    const uint32_t mine = buf + static_cast<uint32_t>(lane & 15) * 128u;
     const uint32_t x = static_cast<uint32_t>(lane & 7);
-    for (int h = 0; h < (A.out_fp32 ? 2 : 1); ++h) {  // 64 columns of bf16, or 32 of fp32, a box
-      if (lane == 0) bulk_wait_group_read0();
-      __syncwarp();
-      if (A.out_fp32) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int i = 4 * c;
-          const float v0 = h == 0 ? a[i] : a[i + 32], v1 = h == 0 ? a[i + 1] : a[i + 33],
-                      v2 = h == 0 ? a[i + 2] : a[i + 34], v3 = h == 0 ? a[i + 3] : a[i + 35];
-          st_shared_v4(mine + ((static_cast<uint32_t>(c) ^ x) << 4), __float_as_uint(v0), __float_as_uint(v1),
-                       __float_as_uint(v2), __float_as_uint(v3));
+    for (int h = 0; h < (F32 ? 2 : 1); ++h) {  // 64 columns of bf16, or 32 of fp32
+      if (32 * h >= ncol) break;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // 16 rows
+        if (row0 + 16 * u >= A.N) break;
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+        if ((lane >> 4) == u) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t dst = mine + ((static_cast<uint32_t>(c) ^ x) << 4);
+            if (F32) {
+              const int i = 32 * h + 4 * c;
+              st_shared_v4(dst, __float_as_uint(a[i]), __float_as_uint(a[i + 1]), __float_as_uint(a[i + 2]),
+                           __float_as_uint(a[i + 3]));
+            } else {
+              st_shared_v4(dst, pack_bf16x2(a[8 * c], a[8 * c + 1]), pack_bf16x2(a[8 * c + 2], a[8 * c + 3]),
+                           pack_bf16x2(a[8 * c + 4], a[8 * c + 5]), pack_bf16x2(a[8 * c + 6], a[8 * c + 7]));
+            }
+          }
         }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          st_shared_v4(mine + ((static_cast<uint32_t>(c) ^ x) << 4), pack_bf16x2(a[8 * c], a[8 * c + 1]),
-                       pack_bf16x2(a[8 * c + 2], a[8 * c + 3]), pack_bf16x2(a[8 * c + 4], a[8 * c + 5]),
-                       pack_bf16x2(a[8 * c + 6], a[8 * c + 7]));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && 32 * h < ncol) {
-        tma_store_2d(&tmOut, buf, col0 + 32 * h, row0);
-        bulk_commit_group();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tmOut, buf, col0 + 32 * h, row0 + 16 * u);
+          bulk_commit_group();
+        }
       }
     }
     return;
   }
-  const int n_rows = min(32, A.N - row0);
-  float* st = reinterpret_cast<float*>(scratch);
+  // 16 rows x 32 words at a time, word w of row k at 32 k + (w + k) % 32: no bank meets twice, in or out
+  uint32_t* st = reinterpret_cast<uint32_t*>(scratch);
 #pragma unroll
-  for (int j = 0; j < COLS; j += 32) {
-    if (j >= ncol) break;
-    // 32 rows x 32 columns, column c of row k at word 32 k + (c + k) % 32: no bank meets twice, in or out
-    __syncwarp();
+  for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+    const int j = 32 * h, n = min(F32 ? 32 : 64, ncol - j);  // columns from j
+    if (n <= 0) break;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) st[lane * 32 + ((i + lane) & 31)] = a[j + i];
-    __syncwarp();
-    const bool in = j + lane < ncol;
-    for (int k = 0; k < n_rows; ++k) {
-      const float v = st[k * 32 + ((lane + k) & 31)];
-      const int64_t o = static_cast<int64_t>(row0 + k) * A.V + col0 + j + lane;
-      if (in) {
-        if (A.out_fp32) static_cast<float*>(A.out)[o] = v;
-        else static_cast<__nv_bfloat16*>(A.out)[o] = __float2bfloat16_rn(v);
+    for (int u = 0; u < 2; ++u) {
+      const int n_rows = min(16, A.N - row0 - 16 * u);
+      if (n_rows <= 0) break;
+      __syncwarp();
+      if ((lane >> 4) == u) {
+        const int k = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          st[k * 32 + ((i + k) & 31)] = F32 ? __float_as_uint(a[j + i]) : pack_bf16x2(a[2 * i], a[2 * i + 1]);
+      }
+      __syncwarp();
+#pragma unroll 4
+      for (int k = 0; k < n_rows; ++k) {
+        const int64_t o = static_cast<int64_t>(row0 + 16 * u + k) * A.V + col0 + j;
+        const uint32_t x = st[k * 32 + ((lane + k) & 31)];
+        if (F32) {
+          if (lane < n) static_cast<uint32_t*>(A.out)[o + lane] = x;
+        } else {
+          // whole words of the output: columns 2 w and 2 w + 1 of the piece, or 2 w + 1 and 2 w + 2, and the single
+          // columns left at its ends
+          uint16_t* out = static_cast<uint16_t*>(A.out) + o;
+          const int odd = static_cast<int>(o & 1);
+          const uint32_t next = __shfl_down_sync(0xffffffffu, x, 1);
+          const uint32_t pair = odd ? (x >> 16) | (next << 16) : x;
+          const int c = 2 * lane + odd;
+          if (c + 1 < n) *reinterpret_cast<uint32_t*>(out + c) = pair;
+          else if (c < n) out[c] = static_cast<uint16_t>(pair & 0xffffu);
+          if (odd && lane == 0) out[0] = static_cast<uint16_t>(x & 0xffffu);
+        }
       }
     }
   }
 }
 
-// OUT: the logits are written out instead of reduced.
-template <bool I8, bool OUT>
+// OUT: the logits are written out, in bf16 (1) or fp32 (2), instead of reduced.
+template <bool I8, int OUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     head_kernel(const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmC,
                 const __grid_constant__ CUtensorMap tmC64, const __grid_constant__ CUtensorMap tmOut,
                 const __grid_constant__ HeadArgs A) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int STAGES = Layout<OUT>::kStages, kScratchWarp = Layout<OUT>::kScratchWarp;
   uint8_t* scratch = base + STAGES * STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + EPI_WARPS * kScratchWarp);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + Layout<OUT>::kBarriers);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + EPI_WARPS * SCRATCH_WARP);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + NUM_BARRIERS);
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bar0 = smem_u32(bars);
@@ -375,7 +393,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const bool rows = row0 < A.N;                // any row of this warp
       const int ncol = min(COLS, t.ncol - part * COLS);  // columns of this warp (none if <= 0)
       const int col0 = t.col + part * COLS;
-      if (!OUT && t.first) {
+      if (OUT == 0 && t.first) {
         m = -INFINITY;
         s = w = 0.f;
         if (A.K == 1) {
@@ -448,8 +466,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
         }
-        if constexpr (OUT) {
-          write_logits(A, tmOut, a, row0, col0, ncol, lane, scratch + (warp - 4) * kScratchWarp);
+        if constexpr (OUT != 0) {
+          write_logits<OUT == 2>(A, tmOut, a, row0, col0, ncol, lane, scratch + (warp - 4) * SCRATCH_WARP);
         } else {
           const bool cut = ncol < COLS;
           if (cut) {
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      if (!OUT && t.last && r < A.N) {
+      if (OUT == 0 && t.last && r < A.N) {
         const int64_t o = static_cast<int64_t>(kHeadParts * t.seg + part) * A.N + r;
         A.part_m[o] = m;
         A.part_s[o] = s;
@@ -602,7 +620,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   }
 
-  if (OUT && warp >= 4) {  // every store of the logits is complete before the kernel ends
+  if (OUT != 0 && warp >= 4) {  // every store of the logits is complete before the kernel ends
     if (lane == 0) bulk_wait_group0();
     __syncwarp();
   }
@@ -1265,16 +1283,16 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(const __nv
   }
 }
 
-template <bool I8, bool OUT>
+template <bool I8, int OUT>
 cudaError_t launch_one(const HeadMaps& M, const HeadArgs& A, bool after_kernel, cudaStream_t s) {
   auto kernel = head_kernel<I8, OUT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<OUT>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if (after_kernel) {
-    e = launch_after_previous(kernel, dim3(A.split.grid), dim3(NUM_THREADS), Layout<OUT>::kBytes, s, M.E, M.C, M.C64, M.out, A);
+    e = launch_after_previous(kernel, dim3(A.split.grid), dim3(NUM_THREADS), SMEM_BYTES, s, M.E, M.C, M.C64, M.out, A);
     if (e != cudaSuccess) return e;
   } else {
-    kernel<<<A.split.grid, NUM_THREADS, Layout<OUT>::kBytes, s>>>(M.E, M.C, M.C64, M.out, A);
+    kernel<<<A.split.grid, NUM_THREADS, SMEM_BYTES, s>>>(M.E, M.C, M.C64, M.out, A);
   }
   note_launches(1);
   return cudaGetLastError();
@@ -1283,9 +1301,11 @@ cudaError_t launch_one(const HeadMaps& M, const HeadArgs& A, bool after_kernel, 
 }  // namespace
 
 cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool after_kernel, cudaStream_t s) {
-  if (A.out != nullptr) return launch_one<true, true>(M, A, after_kernel, s);
-  if (int8) return launch_one<true, false>(M, A, after_kernel, s);
-  return launch_one<false, false>(M, A, after_kernel, s);
+  if (A.out != nullptr) {
+    return A.out_fp32 ? launch_one<true, 2>(M, A, after_kernel, s) : launch_one<true, 1>(M, A, after_kernel, s);
+  }
+  if (int8) return launch_one<true, 0>(M, A, after_kernel, s);
+  return launch_one<false, 0>(M, A, after_kernel, s);
 }
 
 cudaError_t launch_head_picks(HeadPicks P, const HeadFinish& F, bool int8, int sms, cudaStream_t s) {

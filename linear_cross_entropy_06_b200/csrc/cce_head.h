@@ -117,7 +117,7 @@ struct HeadMaps {
   CUtensorMap E;    // box of e_rows rows x 128 bytes
   CUtensorMap C;    // box of 256 rows
   CUtensorMap C64;  // box of 64 rows
-  CUtensorMap out;  // logits, box of 32 rows x 128 bytes (HeadArgs.out_tma)
+  CUtensorMap out;  // logits, box of 16 rows x 128 bytes (HeadArgs.out_tma)
 };
 
 struct HeadFinish {

@@ -455,7 +455,7 @@ cce_status cce_int8_linear(int64_t N, int64_t D, int64_t V, const void* E, const
   A.out_tma = V * out_size % 16 == 0;
   if (A.out_tma)
     CCE_CHECK(cce::make_map(&M.out, out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                            static_cast<size_t>(out_size), out, N, V, static_cast<uint32_t>(128 / out_size), 32));
+                            static_cast<size_t>(out_size), out, N, V, static_cast<uint32_t>(128 / out_size), 16));
   CCE_TRY(cce::launch_head(M, A, true, true, s));
   return CCE_OK;
 }
