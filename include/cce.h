@@ -274,7 +274,7 @@ typedef struct {
   int64_t ignore_index; /* a given token equal to this asks for nothing */
   int32_t num_tokens;   /* given tokens a row, 0 to 32 */
   int32_t top_k;        /* alternatives a row, 0 to 24, at most V */
-  float temperature;    /* > 0 */
+  float temperature;    /* in [1e-6, 1e6] */
   int32_t int8;         /* 1: C is int8 with the scales c_scale; 0: C is bf16 */
   int32_t reserved;     /* must be 0 */
 } cce_logprob_problem;

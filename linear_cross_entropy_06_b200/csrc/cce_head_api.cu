@@ -57,8 +57,8 @@ bool logprobs_ok(const cce_logprob_problem* p, bool set_error) {
   if (p->top_k < 0 || p->top_k > cce::kHeadMaxTop) return bad("top_k must be in [0, 24]");
   if (p->top_k > p->V) return bad("top_k must not exceed V");
   if (p->num_tokens == 0 && p->top_k == 0) return bad("num_tokens and top_k are both 0: nothing to compute");
-  if (!(p->temperature > 0.f && p->temperature < INFINITY)) return bad("temperature must be finite and > 0");
-  if (!(1.f / p->temperature < INFINITY)) return bad("temperature too small");
+  // (beyond these, differences of logits over the temperature leave the range of fp32)
+  if (!(p->temperature >= 1e-6f && p->temperature <= 1e6f)) return bad("temperature must be in [1e-6, 1e6]");
   if (p->reserved != 0) return bad("reserved must be 0");
   return true;
 }

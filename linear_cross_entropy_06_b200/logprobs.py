@@ -18,7 +18,6 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import math
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
@@ -29,6 +28,7 @@ from .ops import _bias_arg, _check, _ptr, _require_cuda
 
 MAX_TOKENS = 32  # given tokens a position
 MAX_TOP = 24     # alternatives a position
+MIN_TEMPERATURE, MAX_TEMPERATURE = 1e-6, 1e6
 
 
 class Int8Rows(NamedTuple):
@@ -112,8 +112,8 @@ def _aligned(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
 
 
 def _check_scalars(top_k: int, V: int, temperature: float) -> None:
-    if not (math.isfinite(temperature) and temperature > 0.0):
-        raise ValueError(f"temperature must be finite and > 0, got {temperature}")
+    if not MIN_TEMPERATURE <= temperature <= MAX_TEMPERATURE:
+        raise ValueError(f"temperature must be in [{MIN_TEMPERATURE}, {MAX_TEMPERATURE}], got {temperature}")
     if not 0 <= top_k <= min(MAX_TOP, V):
         raise ValueError(f"the number of alternatives must be in [0, {min(MAX_TOP, V)}], got {top_k}")
 

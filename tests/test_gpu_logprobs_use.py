@@ -399,6 +399,47 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_survives():
     assert "NAN True" in out.stdout and "RECOVERED True" in out.stdout, out.stdout
 
 
+@pytest.mark.parametrize("T", [2e-6, 1e-3, 1e6])
+def test_extreme_temperatures(device, T):
+    """Nearly one-hot and nearly flat distributions: finite outputs and gradients."""
+    E, C, bias, tok = make(50, 64, 900, 24, device, True, 2)
+    bias[7] = -math.inf
+    lp, H, lse, _, tl, ti = L.cce_logprobs(E, C, tok, 3, bias, T, check=True)
+    ref = torch.log_softmax(logits64(E, C, bias) / T, 1)
+    wanted = (tok != IGNORE) & (tok != 7)
+    want = ref.gather(1, tok.clamp(min=0))
+    dz = (logit_tol(E, C) / T)[:, None]
+    assert ((lp.double() - want).abs() <= 2 * dz + 2.0 ** -18 * (1 + want.abs()))[wanted].all()
+    rH = torch.special.entr(ref.exp()).sum(1)[wanted.any(1)]
+    if T >= 1:
+        assert ((H.double()[wanted.any(1)] - rH).abs() <= 2.0 ** -18 * (1 + rH)).all()
+    assert torch.isfinite(H).all() and (H >= 0).all() and (H <= math.log(900) + 1e-4).all()
+    assert torch.equal(ti, torch.sort(logits64(E, C, bias), dim=1, descending=True, stable=True)[1][:, :3])
+    g, h = torch.randn(50, 2, device=device), torch.randn(50, device=device)
+    out = L.cce_logprobs_backward(E, C, tok, lp, lse, H, None, g, h, 0.0, bias, True, T, check=True)
+    assert all(torch.isfinite(x.float()).all() for x in (out[0], out[1], out[3]))
+
+
+def test_one_vector(device):
+    """e without leading dimensions."""
+    E, C, _, tok = make(1, 64, 300, 25, device, K=1, ignore=0.0)
+    out = lce.linear_logprobs(E[0], C, tok[0, 0], top_k=2)
+    assert out.logprobs.shape == () and out.entropy.shape == () and out.top_ids.shape == (2,)
+    many = lce.linear_logprobs(E[0], C, tok[0])
+    assert many.logprobs.shape == (1,) and many.logprobs[0] == out.logprobs
+    assert lce.linear_top_logprobs(E[0], C, 2).ids.tolist() == out.top_ids.tolist()
+    assert lce.int8_linear(E[0], lce.quantize_int8(C)).shape == (300,)
+
+
+def test_second_derivatives_are_refused(device):
+    E, C, _, tok = make(20, 64, 300, 26, device, K=1, ignore=0.0)
+    e = E.clone().requires_grad_(True)
+    out = lce.linear_logprobs(e, C, tok[:, 0])
+    (ge,) = torch.autograd.grad(out.logprobs.sum(), e, create_graph=True)
+    with pytest.raises(RuntimeError):
+        ge.float().sum().backward()
+
+
 def test_results_do_not_depend_on_the_batch(device):
     """A row's alternatives are the same alone, in a small batch and in a large one (other splits of the work, grouped
     and ungrouped picks)."""

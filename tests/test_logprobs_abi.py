@@ -38,7 +38,7 @@ def backward(lib, p, size=1 << 40, eps=0.0, out=0, **ptr):
 
 @pytest.mark.parametrize("bad", [dict(N=-1), dict(D=0), dict(D=12), dict(V=0), dict(tokens=33), dict(tokens=-1),
                                  dict(top=25), dict(top=-1), dict(tokens=0), dict(V=3, top=4), dict(T=0.0),
-                                 dict(T=-1.0), dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-45),
+                                 dict(T=-1.0), dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-7), dict(T=1e7),
                                  dict(reserved=1), dict(int8=2), dict(int8=1, D=24), dict(int8=1, D=131088),
                                  dict(V=1 << 31)])
 def test_bad_problems_are_refused(lib, bad):
@@ -128,8 +128,9 @@ def test_python_refuses_wrong_types_and_shapes(lib):
         lce.linear_logprobs(e, c, torch.zeros(4, 33, dtype=torch.int64))
     with pytest.raises(lce.CCEError, match="1 to 32 tokens"):
         lce.linear_logprobs(e, c, torch.zeros(4, 0, dtype=torch.int64))
-    with pytest.raises(ValueError, match="temperature"):
-        lce.linear_logprobs(e, c, t, temperature=0.0)
+    for T in (0.0, -1.0, 1e-7, 1e7, float("nan")):
+        with pytest.raises(ValueError, match="temperature"):
+            lce.linear_logprobs(e, c, t, temperature=T)
     with pytest.raises(ValueError, match="alternatives"):
         lce.linear_logprobs(e, c, t, top_k=25)
     with pytest.raises(ValueError, match="alternatives"):
