@@ -942,7 +942,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
   __shared__ unsigned long long best[32];
   __shared__ double exact[32];
   __shared__ unsigned run_mask;
-  wait_for_previous_grid();
+  if (!F.after_dots) wait_for_previous_grid();
   const int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x >> 5) / WARPS;
   if (r >= F.N) return;  // ROWS > 1 only: there nothing below waits for other warps
   const int lane = threadIdx.x & 31, wi = (threadIdx.x >> 5) % WARPS;
@@ -1018,6 +1018,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
     return;
   }
 
+  wait_for_previous_grid();  // the picks' logits
   if (wi == 0) {
     unsigned long long key[kHeadPick];
 #pragma unroll
@@ -1181,6 +1182,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   __shared__ Acc red[WARPS][ROWS * kHeadPick];
   __shared__ int ids[kHeadDotRows];
   wait_for_previous_grid();
+  let_next_grid_start();  // the head kernel has ended: the finish may join its statistics meanwhile
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t pitch = static_cast<int64_t>(P.D) * (I8 ? 1 : 2);  // a multiple of 16 bytes
   const int nitems = kGrouped ? P.done[1] : P.N * P.wanted;
@@ -1332,7 +1334,8 @@ cudaError_t launch_head_picks(HeadPicks P, const HeadFinish& F, bool int8, int s
   return launch_head_finish(F, s);
 }
 
-cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s) {
+cudaError_t launch_head_finish(HeadFinish F, cudaStream_t s) {
+  F.after_dots = F.top_k > 0 ? 1 : 0;
   // A block of eight warps per row where a row has very many segments (one or two row blocks share the machine), so
   // that they are read at once; else two where alternatives are to be ordered; else a warp per row, four rows a block.
   cudaError_t e;

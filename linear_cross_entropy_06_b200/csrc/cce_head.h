@@ -142,6 +142,7 @@ struct HeadFinish {
   const float* logits;  // of the picks
   int wanted;
   int top_k;
+  int after_dots;    // it follows head_dots_kernel, and may read what the head kernel wrote before that has ended
   float* logprobs;   // [N, K]
   float* entropy;    // [N]
   float* lse;        // [N]
@@ -159,7 +160,7 @@ inline bool picks_grouped(int64_t rows) { return rows > kUngroupedRows; }
 // These two follow a kernel of the same call on s. With picks_grouped the counters are zero before.
 // The first also launches the finish.
 cudaError_t launch_head_picks(HeadPicks P, const HeadFinish& F, bool int8, int sms, cudaStream_t s);
-cudaError_t launch_head_finish(const HeadFinish& F, cudaStream_t s);
+cudaError_t launch_head_finish(HeadFinish F, cudaStream_t s);
 cudaError_t launch_head_tokens(const int64_t* tokens, int N, int K, int V, int64_t ignore_index, int* tok_t,
                                cudaStream_t s);
 // Rows of 8-bit integers: scale = max |x| / 127, q = x / scale to the nearest integer.
