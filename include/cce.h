@@ -279,9 +279,10 @@ typedef struct {
   int32_t reserved;     /* must be 0 */
 } cce_logprob_problem;
 
-/* Bytes of device workspace cce_logprobs() needs (0 for a bad problem). Of the order of N * 12 bytes a
- * segment (a row block's share of one SM, 2 * (148 / row blocks + 1) of them), 24 times that with
- * alternatives, and with int8 E once more: never anything of size N * V. */
+/* Bytes of device workspace cce_logprobs() needs (0 for a bad problem): 48 bytes a row and segment (a row
+ * block's share of one SM, at most 148 / row blocks + 2 of them), 4 to 8 a row and given token, E in 8
+ * bits with int8, and with alternatives V / 4 + 2700 bytes a row of at most 4096 rows (longer batches are
+ * taken so many rows at a time): never anything of size N * V. */
 CCE_API size_t cce_logprobs_workspace_size(const cce_logprob_problem* p);
 
 /*
@@ -313,10 +314,10 @@ CCE_API size_t cce_logprobs_backward_workspace_size(const cce_logprob_problem* p
  */
 CCE_API cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, const void* C, const void* bias,
                                          const int64_t* tokens, const float* logprobs, const float* lse,
-                                         const float* entropy, const float* tile_max, const float* grad_logprobs, const float* grad_entropy,
-                                         float filter_eps, void* dE, void* dC, void* dbias, int32_t out_fp32,
-                                         int64_t* filtered_tiles, void* workspace, size_t workspace_bytes,
-                                         cce_stream_t stream);
+                                         const float* entropy, const float* tile_max, const float* grad_logprobs,
+                                         const float* grad_entropy, float filter_eps, void* dE, void* dC,
+                                         void* dbias, int32_t out_fp32, int64_t* filtered_tiles, void* workspace,
+                                         size_t workspace_bytes, cce_stream_t stream);
 
 /* Rows of x (device bf16 [rows, D]) as 8-bit integers q [rows, D] and scales fp32 [rows]. A row of
  * zeros gets scale 0; a row with an infinity or a NaN gets the scale NaN. */

@@ -2,8 +2,9 @@
 
 The compute runs in ``libcce.so`` (hand-written CUDA for sm_100a behind a C ABI,
 declared in ``include/cce.h``). ``ops`` is the thin ctypes binding and the
-autograd wrapper of the loss, ``logprobs`` that of the log-probabilities, alternatives and 8-bit logits; importing this package does not load the library, the first
-call does, and fails loudly if it is missing.
+autograd wrapper of the loss, ``logprobs`` that of the log-probabilities, alternatives and 8-bit
+logits; importing this package does not load the library, the first call does, and fails loudly if it
+is missing.
 """
 from .logprobs import (  # noqa: F401
     Int8Rows,

@@ -587,9 +587,10 @@ size_t logprobs_backward_bytes(const cce_problem* p, int K, int32_t out_fp32) {
   return carve_logprob(p, K, carve_split(p, out_fp32, nullptr).bytes, nullptr).bytes;
 }
 
-cce_status logprobs_backward(const cce_problem* p, const LogprobGrads& g, const void* E, const void* C, const void* bias,
-                             const float* tile_max, float filter_eps, void* dE, void* dC, void* dbias, int32_t out_fp32,
-                             int64_t* filtered_tiles, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+cce_status logprobs_backward(const cce_problem* p, const LogprobGrads& g, const void* E, const void* C,
+                             const void* bias, const float* tile_max, float filter_eps, void* dE, void* dC, void* dbias,
+                             int32_t out_fp32, int64_t* filtered_tiles, void* workspace, size_t workspace_bytes,
+                             cudaStream_t s) {
   if (!problem_ok(p, true)) return CCE_ERR_INVALID_ARG;
   return backward_split(p, E, C, bias, g.tokens, g.lse, tile_max, filtered_tiles, nullptr, filter_eps, dE, dC, dbias,
                         out_fp32, filtered_tiles, workspace, workspace_bytes, s, &g);

@@ -185,7 +185,9 @@ __device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddep
 
 // Lets the next kernel of the stream, if launched with launch_after_previous(), start as soon as every block has
 // called this: its blocks then set themselves up while this kernel runs, and wait in wait_for_previous_grid().
-__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void let_next_grid_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // Bulk copy of `bytes` (a multiple of 16) from shared memory to global memory, both 16-byte aligned.
 __device__ __forceinline__ void bulk_store(void* gdst, uint32_t src, uint32_t bytes) {

@@ -16,11 +16,13 @@
 //   warps 4..19  epilogue, four warps for each 32 rows (one for each 64 columns of the tile): a thread owns
 //                64 logits of one row, in registers. Four warps a scheduler hide the latency of tensor memory
 //                and of the exponentials; eight warps with 128 logits each were bound by it (2048 x 2048 x
-//                128256: 844 us).
+//                128256: 844 us against 785).
+// What bounds it: the delivery of operands from L2, 48 KB a step of 128 x 256 x 64 (2048 x 2048 x 128256: tensor pipe
+// 79 % busy at 1.53 GHz, 770 us, 1397 TFLOP/s); with few rows reading C (one row of D = 4096: 6.1 TB/s).
 // Sums over K: the tensor cores add into their fp32 accumulator without rounding to nearest, so a long sum
 // drifts towards zero (D = 4096, logits of 11: -5e-5, sixteen times what fp32 sums lose). The accumulator is
-// therefore handed over every kb_chunk K-blocks (512 values of K) and the parts are added in registers, rounded
-// to nearest: two tensor-memory buffers alternate by parts, and the drift falls with the parts' number.
+// therefore handed over every kb_chunk K-blocks (512 or 256 values of K) and the parts are added in registers,
+// rounded to nearest: two tensor-memory buffers alternate by parts, and the drift falls with the parts' number.
 // 8-bit products are exact in 32-bit integers, so they keep one part.
 #include <algorithm>
 #include <type_traits>
@@ -44,7 +46,7 @@ constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int COLS = BN / (EPI_WARPS / 4);  // columns of a thread
 constexpr int TMEM_COLS = 512;
 constexpr int NUM_BARRIERS = 2 * STAGES + 4 + 1;
-constexpr int SCRATCH_WARP = 2048;  // of each epilogue warp: a piece of the logits on its way out (16 rows of 128 bytes)
+constexpr int SCRATCH_WARP = 2048;  // of each epilogue warp: a piece of the logits going out (16 rows of 128 bytes)
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * SCRATCH_WARP + NUM_BARRIERS * 8 + 16;
 static_assert(SMEM_BYTES <= 232448, "fits the 227 KB opt-in shared memory of an SM");
 static_assert(COLS == kSubTile && COLS == 4 * kHeadPick, "a thread's columns are one saved maximum, and four picks");
@@ -657,7 +659,8 @@ __device__ double exact_logit(const HeadFinish& F, int64_t r, int col, int lane)
       p = __dp4a(static_cast<int>(x.w), static_cast<int>(y.w), p);
       acc += p;
     }
-    z = warp_sum_f64(static_cast<double>(acc)) * static_cast<double>(F.e_scale[r]) * static_cast<double>(F.c_scale[col]);
+    z = warp_sum_f64(static_cast<double>(acc)) * static_cast<double>(F.e_scale[r]) *
+        static_cast<double>(F.c_scale[col]);
   } else {
     double acc = 0.0;
     const __nv_bfloat16* e = F.E + r * F.D;
@@ -875,7 +878,8 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 5 : 1)
   }
   if (w == 0) {
     const int count = sieve ? sifted : 32 * WARPS;
-    const int m = count <= 64 ? warp_best<2>(keys, count, W, lane, keys) : warp_best<kKeys / 32>(keys, count, W, lane, keys);
+    const int m = count <= 64 ? warp_best<2>(keys, count, W, lane, keys)
+                              : warp_best<kKeys / 32>(keys, count, W, lane, keys);
     const int unit = lane < m ? key_column(keys[lane]) : -1;
     P.pick[static_cast<int64_t>(r) * 32 + lane] = unit;
     if (P.grouped) {
@@ -1026,8 +1030,9 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
       const int j = 2 * i + (lane >> 4);  // two picks a step
       const int unit = j < F.wanted ? F.pick[r * 32 + j] : -1;
       const int c = unit * kHeadPick + (lane & 15);
-      key[i] = unit >= 0 && c < F.V ? make_key(F.logits[(r * 32 + j) * kHeadPick + (lane & 15)], static_cast<uint32_t>(c))
-                                    : 0ull;
+      key[i] = unit >= 0 && c < F.V
+                   ? make_key(F.logits[(r * 32 + j) * kHeadPick + (lane & 15)], static_cast<uint32_t>(c))
+                   : 0ull;
     }
     const unsigned long long bound = warp_bound(key, 32);
     best[lane] = 0;
@@ -1079,7 +1084,8 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
   }
   if (place < F.top_k && in) {
     const float lp = m == -INFINITY ? -INFINITY
-                                    : static_cast<float>((zx - static_cast<double>(m)) * static_cast<double>(F.inv_t)) - ln_s;
+                                    : static_cast<float>((zx - static_cast<double>(m)) *
+                                                         static_cast<double>(F.inv_t)) - ln_s;
     F.top_logprobs[r * F.top_k + place] = s != s ? nan : lp;
     F.top_ids[r * F.top_k + place] = col;
   }
@@ -1105,8 +1111,8 @@ __device__ __forceinline__ void mma_16x8(int (&c)[4], uint32_t a0, uint32_t a1, 
 // A work item: 16 columns x up to 64 gathered rows. The operands are the rows themselves, read 64 bytes a row and
 // step: the WARPS warps take the steps in turn and their sums are added through shared memory. Four warps, and four
 // blocks an SM, where there are many items (2048 rows of D = 2048: 116 us, 120 with eight warps and two blocks),
-// eight where there are few and each should be done soon. A lane's 16 bytes
-// of a row feed two instructions whose K positions are the same bytes of both operands, so nothing is rearranged.
+// eight where there are few and each should be done soon. A lane's 16 bytes of a row feed two instructions whose K
+// positions are the same bytes of both operands, so nothing is rearranged.
 // Rows picked by index suit neither a TMA box nor an M = 128 tile (a pick has 7 rows of 2048 on average); the warp
 // instruction's 16-row tile wastes little, and the kernel is bound by reading C once.
 constexpr int kDotStep = 64;  // bytes of a row a step

@@ -21,13 +21,13 @@ constexpr int kHeadPick = 16;      // columns of a pick: the unit whose largest 
 constexpr int kHeadDotRows = 64;   // rows of a work item of head_dots_kernel
 constexpr int kHeadSlab = 4096;    // rows whose alternatives are found at a time: bounds their workspace
 
+constexpr int kHeadMaxGrid = 148;  // SMs of a B200
+
 // How the logit tiles are split over the blocks of the grid. Row blocks are taken in `ngroups` groups of
 // nearly equal size. A group's work is the list of its units (`unit` vocabulary columns of one row
 // block), row block by row block; part c of the P = min(grid, units) parts gets the units
-// [c U / P, (c + 1) U / P), and one block walks it. What a block gets of one row block is a segment: it keeps the softmax
-// statistics (and the best alternatives) of the segment on chip and writes them once.
-constexpr int kHeadMaxGrid = 148;  // SMs of a B200
-
+// [c U / P, (c + 1) U / P), and one block walks it. What a block gets of one row block is a segment: it
+// keeps the softmax statistics of the segment on chip and writes them once.
 struct HeadSplit {
   int nb;       // row blocks
   int nu;       // units of a row block
@@ -36,8 +36,8 @@ struct HeadSplit {
   int grid;     // at most kHeadMaxGrid
   // Which part a block takes, for the smaller groups and for those with one row block more: by where in the
   // vocabulary the part starts. Neighbouring blocks (two SMs that share a path to L2) then walk the same columns of
-  // C on different row blocks, and what both load at a time crosses from L2 once (2048 x 2048 x 128256: 334
-  // million sectors in the parts' own order, where neighbours share rows of E instead).
+  // C on different row blocks, and what both load at a time crosses from L2 once (2048 x 2048 x 128256: 256
+  // million sectors, against 334 million in the parts' own order, where neighbours share rows of E instead).
   uint8_t order[2][kHeadMaxGrid];
 
   __host__ __device__ int group_begin(int g) const {
@@ -154,8 +154,10 @@ struct HeadFinish {
 
 cudaError_t launch_head(const HeadMaps& M, const HeadArgs& A, bool int8, bool after_kernel, cudaStream_t s);
 // Up to this many rows every pick is computed for its row alone: the rows' picks are then nearly all different, and
-// bringing equal ones together costs more (a launch, and a chain of atomics in the one before) than it saves.
-constexpr int kUngroupedRows = 64;
+// bringing equal ones together costs more (a launch, and a chain of atomics in the one before) than it saves. Alone
+// and together, 20 alternatives, us: 16 x 4096 x 128256: 211, 222; 96 x 1024 x 50257: 63, 68; 128 x 2048 x 128256:
+// 162, 166; 160 x 2048 x 128256: 211, 211; 200 x 2048 x 50257: 149, 128.
+constexpr int kUngroupedRows = 128;
 inline bool picks_grouped(int64_t rows) { return rows > kUngroupedRows; }
 // These two follow a kernel of the same call on s. With picks_grouped the counters are zero before.
 // The first also launches the finish.

@@ -65,10 +65,10 @@ bool logprobs_ok(const cce_logprob_problem* p, bool set_error) {
 
 // The split of the logit tiles over `sms` blocks. With at least kWideTiles tiles a block, units of a whole tile: a
 // block's share is uneven by at most one tile in that many, and the walk can be aligned. With fewer, units of 64
-// columns, so that the blocks' shares of C stay even: one row block of 128256 columns on 148 SMs gets 13.5 units (at
-// most 14) instead of 3.4 tiles (at most 4).
+// columns, so that the blocks' shares stay even. Whole tiles and 64 columns, us: 4.3 tiles a block (513 x 1032 x
+// 32003) 66, 62; 16 (1500 x 1024 x 50257) 157, 163; 54 (2048 x 2048 x 128256, 8-bit logits) 512, 576; between 6 and
+// 16 tiles of 2048-long rows nothing within the noise of 3 %.
 constexpr int64_t kWideTiles = 12;
-constexpr int kEvenPercent = 94;
 
 cce::HeadSplit make_split(int64_t N, int64_t V, int sms) {
   cce::HeadSplit S;
@@ -79,14 +79,12 @@ cce::HeadSplit make_split(int64_t N, int64_t V, int sms) {
   const bool wide = rows * ceil_div(V, cce::kHeadBN) >= kWideTiles * sms;
   S.unit = wide ? cce::kHeadBN : cce::kHeadUnit;
   S.nu = static_cast<int>(ceil_div(V, S.unit));
-  // Small problems: the same number of parts for every row block, where that leaves few SMs idle. The row blocks'
-  // parts then start at the same columns, and each column of C is read from HBM once (777 x 1288 x 50257: 138 us
-  // against 173 with even shares for all SMs). With wide units the walk itself is aligned (for_tiles), and idle SMs
-  // cost more than that leaves to gain (2048 x 2048 x 128256: 906 us against 889 on the same machine).
-  if (!wide && S.ngroups == 1) {
-    const int even = sms / S.nb * S.nb;
-    if (even * 100 >= kEvenPercent * sms) S.grid = even;
-  }
+  // Small problems: the same number of parts for every row block. The row blocks' parts then start at the same
+  // columns, and each column of C is read from HBM once (777 x 1288 x 50257: 138 us against 173 with even shares for
+  // all SMs; with 15 row blocks, which leave the most SMs idle, 13 of 148: 1920 x 1024 x 16000 62 against 66). With
+  // wide units the walk itself is aligned (for_tiles), and idle SMs cost more than that leaves to gain (2048 x 2048 x
+  // 128256: 906 us against 889 on the same machine).
+  if (!wide && S.ngroups == 1 && sms >= S.nb) S.grid = sms / S.nb * S.nb;
   return S;
 }
 

@@ -53,9 +53,10 @@ struct LogprobGrads {
   const float* g_entropy;     // [N] or null
 };
 size_t logprobs_backward_bytes(const cce_problem* p, int K, int32_t out_fp32);
-cce_status logprobs_backward(const cce_problem* p, const LogprobGrads& g, const void* E, const void* C, const void* bias,
-                             const float* tile_max, float filter_eps, void* dE, void* dC, void* dbias, int32_t out_fp32,
-                             int64_t* filtered_tiles, void* workspace, size_t workspace_bytes, cudaStream_t s);
+cce_status logprobs_backward(const cce_problem* p, const LogprobGrads& g, const void* E, const void* C,
+                             const void* bias, const float* tile_max, float filter_eps, void* dE, void* dC, void* dbias,
+                             int32_t out_fp32, int64_t* filtered_tiles, void* workspace, size_t workspace_bytes,
+                             cudaStream_t s);
 
 }  // namespace cce
 

@@ -232,8 +232,8 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     with _on(dev):
         _check(lib.cce_logprobs_backward(p, E.data_ptr(), rows.data_ptr(), _ptr(bias), tokens.data_ptr(),
                                          logprobs.data_ptr(), lse.data_ptr(), entropy.data_ptr(), _ptr(tile_max),
-                                         _ptr(g_lp), _ptr(g_h), float(filter_eps), dE.data_ptr(), dC.data_ptr(), _ptr(db), mode,
-                                         filtered.data_ptr(), ws.data_ptr(), ws_bytes, _stream(dev)))
+                                         _ptr(g_lp), _ptr(g_h), float(filter_eps), dE.data_ptr(), dC.data_ptr(),
+                                         _ptr(db), mode, filtered.data_ptr(), ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
     return (dE, dC, filtered) + ((db,) if want_dbias else ())
