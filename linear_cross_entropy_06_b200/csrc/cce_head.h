@@ -22,6 +22,7 @@ constexpr int kHeadDotRows = 64;   // rows of a work item of head_dots_kernel
 constexpr int kHeadSlab = 4096;    // rows whose alternatives are found at a time: bounds their workspace
 
 constexpr int kHeadMaxGrid = 148;  // SMs of a B200
+constexpr int kNoToken = 0x7fffffff;  // behind every column
 
 // How the logit tiles are split over the blocks of the grid. Row blocks are taken in `ngroups` groups of
 // nearly equal size. A group's work is the list of its units (`unit` vocabulary columns of one row
@@ -69,10 +70,10 @@ struct HeadArgs {
   const float* e_scale;       // [N], [V]: scales of 8-bit operands
   const float* c_scale;
   const int64_t* tokens;      // [N, K]
-  const int* tok_t;           // [K, N], -1 for none (K > 1)
+  const int* tok_t;           // [K, N]: each row's tokens in ascending order, kNoToken for none (K > 1)
   int64_t ignore_index;
   int K;
-  float* zt;        // [K, N]: logits of the given tokens
+  float* zt;        // [K, N]: logits of the given tokens, in the order of tok_t
   float* tile_max;  // [ceil(V / 64), max_pitch]: largest y of each 64 columns, or null
   int64_t max_pitch;
   float* pick_max;  // [N, picks]: largest logit of each pick, or null

@@ -115,7 +115,7 @@ struct HeadWs {
   cce::WsHeader* hdr;
   int* counters;   // HeadPicks.done and .count, directly behind the header
   size_t counter_bytes;
-  int* tok_t;      // [K, N] (K > 1)
+  int* tok_t;      // [K, N] (K > 1), see HeadArgs
   float* zt;       // [K, N]
   float* part_m;   // [4 segments, N] each
   float* part_s;

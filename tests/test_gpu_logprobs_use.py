@@ -517,3 +517,28 @@ def test_a_teacher_and_a_student(device):
     nll = ops.linear_cross_entropy(E, C, teacher.ids[:, 0], reduction="none")
     lp = lce.linear_logprobs(E, C, teacher.ids[:, 0]).logprobs
     assert (nll + lp).abs().max() <= 2 * logit_tol(E, C).max().item() + 2.0 ** -18 * (1 + lp.abs().max().item())
+
+
+@pytest.mark.parametrize("N,V", [(700, 80001), (300, 5000), (2100, 131)])
+def test_many_tokens_are_met_wherever_they_lie(device, N, V):
+    """32 tokens a position, apart, side by side, equal, at both ends and none at all, in any order: each has the
+    log-probability that it has alone (the same logit, the same sums: to the bit). 700 x 80001 walks its columns from
+    the middle of a share on and turns round."""
+    gen = torch.Generator().manual_seed(N + V)
+    E = torch.randn(N, 64, generator=gen).bfloat16().to(device)
+    C = torch.randn(V, 64, generator=gen).bfloat16().to(device)
+    tok = torch.randint(0, V, (N, 32), generator=gen)
+    tok[::3, :20] = torch.randint(0, V - 20, (len(tok[::3]), 1), generator=gen) + torch.randperm(20, generator=gen)
+    tok[1::3, 5:9] = tok[1::3, 4:5]
+    tok[:, 10] = V - 1
+    tok[:, 11] = 0
+    tok[torch.rand(N, 32, generator=gen) < 0.1] = -100
+    tok[17] = -100
+    tok = tok.to(device)
+    many = lce.linear_logprobs(E, C, tok)
+    for k in range(32):
+        alone = lce.linear_logprobs(E, C, tok[:, k])
+        assert torch.equal(many.logprobs[:, k], alone.logprobs)
+        asks = (tok[:, k] != -100)
+        assert torch.equal(many.entropy[asks], alone.entropy[asks])
+    assert many.entropy[17] == 0 and (many.logprobs[17] == 0).all()
