@@ -179,7 +179,7 @@ __device__ void tile_flags_unit(const PlanArgs& A, int group, int b, int t0) {
     for (int k = 0; k < A.K; ++k) {
       const int id = A.tok[static_cast<int64_t>(k) * A.N + r];
       const int64_t h = id / kSubTile - j0;
-      if (id >= 0 && h >= 0 && h < 2 * kFlagTiles) mine |= 1u << h;
+      if (h >= 0 && h < 2 * kFlagTiles) mine |= 1u << h;
     }
   }
   float mt[2 * kFlagTiles];
@@ -750,13 +750,13 @@ __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid
     const bool fine = lse != -INFINITY;  // a NaN goes on as NaN
     float sum = 0.f, lp = 0.f;
     bool any = false;
-    int tok = -1;
+    int tok = kNoToken;
     if (lane < P.K) {
       const int64_t id = P.tokens[static_cast<int64_t>(r) * P.K + lane];
       any = id != P.ignore_index && id >= 0 && id < P.V;
       sum = any && fine && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + lane] : 0.f;
-      tok = any && fine ? static_cast<int>(id) : -1;
-      if (tok >= 0) lp = P.logprobs[static_cast<int64_t>(r) * P.K + lane];
+      tok = any && fine ? static_cast<int>(id) : kNoToken;
+      if (tok != kNoToken) lp = P.logprobs[static_cast<int64_t>(r) * P.K + lane];
     }
     any = __any_sync(0xffffffffu, any) && fine;
     const float g = sum * P.inv_t;
@@ -770,9 +770,14 @@ __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid
     const float s = P.K == 1 && entry > 1e-30f && entry < 1e30f
                         ? __uint_as_float((__float_as_uint(entry) & 0x7fffffu) | 0x3f800000u)
                         : 1.f;
+    int place = 0;  // of the lane's token among the row's, in ascending order
+    for (int k = 0; k < P.K; ++k) {
+      const int other = __shfl_sync(0xffffffffu, tok, k);
+      place += other < tok || (other == tok && k < lane) ? 1 : 0;
+    }
     if (lane < P.K) {
-      P.tok[static_cast<int64_t>(lane) * P.N + r] = tok;
-      P.tok_g[static_cast<int64_t>(lane) * P.N + r] = g / s;
+      P.tok[static_cast<int64_t>(place) * P.N + r] = tok;
+      P.tok_g[static_cast<int64_t>(place) * P.N + r] = g / s;
     }
     if (lane == 0) {
       P.coef[r] = coef / s;

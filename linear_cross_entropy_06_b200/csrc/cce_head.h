@@ -8,6 +8,8 @@
 
 #include <stdint.h>
 
+#include "cce_internal.h"
+
 namespace cce {
 
 constexpr int kHeadBM = 128;       // rows of a logit tile
@@ -22,7 +24,6 @@ constexpr int kHeadDotRows = 64;   // rows of a work item of head_dots_kernel
 constexpr int kHeadSlab = 4096;    // rows whose alternatives are found at a time: bounds their workspace
 
 constexpr int kHeadMaxGrid = 148;  // SMs of a B200
-constexpr int kNoToken = 0x7fffffff;  // behind every column
 
 // How the logit tiles are split over the blocks of the grid. Row blocks are taken in `ngroups` groups of
 // nearly equal size. A group's work is the list of its units (`unit` vocabulary columns of one row

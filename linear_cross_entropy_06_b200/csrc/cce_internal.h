@@ -14,6 +14,7 @@ namespace cce {
 // Forward tile: 128 rows x 256 vocabulary columns, K in blocks of 64 (one 128-byte swizzle row).
 constexpr int kFwdBM = 128;
 constexpr int kFwdBN = 256;
+constexpr int kNoToken = 0x7fffffff;  // in lists of given tokens: none (behind every column)
 constexpr int kSubTile = 64;  // vocabulary width of one saved tile max (and of a skip-rule unit)
 
 // Backward tile: 128 rows x 128 vocabulary columns (a gradient tile and the unit of the work lists),
@@ -196,8 +197,8 @@ struct BwdArgs {
   // Gradient of log-probabilities and entropy instead of the loss (lp_coef not null; see LogprobPrep)
   const float* lp_coef;
   const float* lp_coef_log;
-  const int* lp_tok;      // [lp_k, N]
-  const float* lp_tok_g;  // [lp_k, N]
+  const int* lp_tok;      // [lp_k, N], each row's in ascending order, kNoToken for none
+  const float* lp_tok_g;  // [lp_k, N], in the same order
   int lp_k;
   float lp_inv_t;         // 1 / temperature
   const float* lp_scale;  // [N]: see LogprobPrep
@@ -238,7 +239,7 @@ struct PlanArgs {
   int* bar;                // grid barrier counter, zero at launch
   int* err;
   uint64_t timeout_ns;
-  const int* tok;          // [K, N] given tokens (-1: none) whose units are always kept, or null
+  const int* tok;          // [K, N] given tokens (kNoToken: none) whose units are always kept, or null
   int K;
   int de_split;            // BwdArgs.de_split (a plan that skips has 1)
   int inject_stall;        // test hook: block 0 leaves before the first grid barrier, whose wait then runs out
@@ -324,8 +325,8 @@ cudaError_t launch_fill_zero(void* dst, int64_t bytes, cudaStream_t s);
 // What the backward of the log-probabilities needs before its plan (cce_bwd_plan.cu, one launch). With
 // y = z / T, lp_k = y_{t_k} - lse, p = softmax(y) and the gradients g_k of lp_k and h of the entropy H:
 //   dz_v = (1 / T) (sum_k g_k [v = t_k] - p_v (sum_k g_k + h H + h ln p_v)).
-// Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and tok_g[k] = g_k / T for the tokens
-// tok[k] (-1: ignored), all divided by the row's scale s. A row that asks for nothing, or has no finite
+// Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and tok_g = g_k / T for the tokens tok
+// (in ascending order; kNoToken, behind the others, for ignored ones), all divided by the row's scale s. A row that asks for nothing, or has no finite
 // logit, gets zeros and lse = +inf (G = 0).
 // The scale: G goes through bf16, and with one token a row dE of a row is mostly that token's entry times
 // its row of C, so an error of that one entry is an error of the whole row. With s in [1, 2) the

@@ -519,26 +519,45 @@ def test_a_teacher_and_a_student(device):
     assert (nll + lp).abs().max() <= 2 * logit_tol(E, C).max().item() + 2.0 ** -18 * (1 + lp.abs().max().item())
 
 
-@pytest.mark.parametrize("N,V", [(700, 80001), (300, 5000), (2100, 131)])
-def test_many_tokens_are_met_wherever_they_lie(device, N, V):
-    """32 tokens a position, apart, side by side, equal, at both ends and none at all, in any order: each has the
-    log-probability that it has alone (the same logit, the same sums: to the bit). 700 x 80001 walks its columns from
-    the middle of a share on and turns round."""
-    gen = torch.Generator().manual_seed(N + V)
-    E = torch.randn(N, 64, generator=gen).bfloat16().to(device)
-    C = torch.randn(V, 64, generator=gen).bfloat16().to(device)
+def scattered_tokens(N, V, gen):
+    """32 tokens a position: apart, 20 side by side in every third row, equal ones in the next, one at either end, in
+    any order, some asking for nothing, and all of them in row 17."""
     tok = torch.randint(0, V, (N, 32), generator=gen)
     tok[::3, :20] = torch.randint(0, V - 20, (len(tok[::3]), 1), generator=gen) + torch.randperm(20, generator=gen)
     tok[1::3, 5:9] = tok[1::3, 4:5]
     tok[:, 10] = V - 1
     tok[:, 11] = 0
-    tok[torch.rand(N, 32, generator=gen) < 0.1] = -100
-    tok[17] = -100
-    tok = tok.to(device)
+    tok[torch.rand(N, 32, generator=gen) < 0.1] = IGNORE
+    tok[17] = IGNORE
+    return tok
+
+
+@pytest.mark.parametrize("N,V", [(700, 80001), (300, 5000), (2100, 131)])
+def test_many_tokens_are_met_wherever_they_lie(device, N, V):
+    """Each of 32 tokens has the log-probability that it has alone (the same logit, the same sums: to the bit).
+    700 x 80001 walks its columns from the middle of a share on and turns round."""
+    gen = torch.Generator().manual_seed(N + V)
+    E = torch.randn(N, 64, generator=gen).bfloat16().to(device)
+    C = torch.randn(V, 64, generator=gen).bfloat16().to(device)
+    tok = scattered_tokens(N, V, gen).to(device)
     many = lce.linear_logprobs(E, C, tok)
     for k in range(32):
         alone = lce.linear_logprobs(E, C, tok[:, k])
         assert torch.equal(many.logprobs[:, k], alone.logprobs)
-        asks = (tok[:, k] != -100)
+        asks = tok[:, k] != IGNORE
         assert torch.equal(many.entropy[asks], alone.entropy[asks])
     assert many.entropy[17] == 0 and (many.logprobs[17] == 0).all()
+
+
+@pytest.mark.parametrize("N,V", [(300, 5000), (150, 131)])
+def test_gradients_of_many_tokens(device, N, V):
+    E, C, bias, _ = make(N, 64, V, 3 * N + V, device, True, 1)
+    gen = torch.Generator().manual_seed(V)
+    tok = scattered_tokens(N, V, gen).to(device)
+    g = torch.randn(N, 32, generator=gen).to(device)
+    h = torch.randn(N, generator=gen).to(device)
+    lp, H, lse, *_ = L.cce_logprobs(E, C, tok, 0, bias, 0.7)
+    out = L.cce_logprobs_backward(E, C, tok, lp, lse, H, None, g, h, bias=bias, temperature=0.7, out_fp32=ops.OUT_FP32)
+    ref, tol = grad_reference(E, C, bias, tok, 0.7, g, h)
+    check_grads((out[0], out[1], out[3]), ref, tol)
+    assert (out[0][17] == 0).all()
