@@ -561,3 +561,19 @@ def test_gradients_of_many_tokens(device, N, V):
     ref, tol = grad_reference(E, C, bias, tok, 0.7, g, h)
     check_grads((out[0], out[1], out[3]), ref, tol)
     assert (out[0][17] == 0).all()
+
+
+def test_many_tokens_of_a_long_batch_with_alternatives(device):
+    """Rows are taken a slab at a time there, their tokens too."""
+    N, V = 4500, 700
+    E, C, _, _ = make(N, 64, V, 29, device, K=1)
+    tok = scattered_tokens(N, V, torch.Generator().manual_seed(2)).to(device)
+    lp, H, lse, _, tl, ti = L.cce_logprobs(E, C, tok, 3, check=True)
+    check_logprobs(E, C, None, tok, 1.0, lp, H)
+    check_top(E, C, None, 3, 1.0, lce.TopLogprobs(tl, ti))
+    q = lce.quantize_int8(C)
+    lp8, H8, *_ = L.cce_logprobs(E, q, tok, 3, check=True)
+    alone, Ha, *_ = L.cce_logprobs(E, q, tok, check=True)
+    # the same logits (8-bit products are exact); only the order of the statistics' sums differs
+    assert ((lp8 - alone).abs() <= 2.0 ** -18 * (1 + alone.abs())).all()
+    assert ((H8 - Ha).abs() <= 2.0 ** -18 * (1 + math.log(V))).all()
