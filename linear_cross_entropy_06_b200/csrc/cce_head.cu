@@ -715,12 +715,12 @@ __device__ double exact_logit(const HeadFinish& F, int64_t r, int col, int lane)
 //   head_finish_kernel   the best of a row's 16 W logits, in order
 // ---------------------------------------------------------------------------------------------
 
-// The want-th largest of a warp's 32 R keys (R in each lane's registers; 0 is below every key), or the smallest of
-// them that is not 0 where there are fewer: bisection on the keys' bits, stopped as soon as a bound has exactly
-// `want` keys at or above it. Each step is R comparisons and one sum over the warp, independent of the data's order
-// (inserting into a sorted list across the lanes takes a chain of shuffles for every key that passes).
+// A bound that `want` to `most` of a warp's 32 R keys reach (R in each lane's registers; 0 is below every key), or the
+// smallest of them that is not 0 where there are fewer: bisection on the keys' bits, stopped as soon as there is one
+// (at the want-th largest at the latest). Each step is R comparisons and one sum over the warp, independent of the
+// data's order (inserting into a sorted list across the lanes takes a chain of shuffles for every key that passes).
 template <int R>
-__device__ __forceinline__ unsigned long long warp_bound(const unsigned long long (&key)[R], int want) {
+__device__ __forceinline__ unsigned long long warp_bound(const unsigned long long (&key)[R], int want, int most) {
   uint32_t hi = 0, lo = 0xffffffffu;  // upper words: of the largest key, and of the smallest that is not 0
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -738,7 +738,7 @@ __device__ __forceinline__ unsigned long long warp_bound(const unsigned long lon
 #pragma unroll
     for (int i = 0; i < R; ++i) n += static_cast<uint32_t>(key[i] >> 32) >= mid ? 1 : 0;
     n = __reduce_add_sync(0xffffffffu, n);
-    if (n == want) return static_cast<unsigned long long>(mid) << 32;
+    if (n >= want && n <= most) return static_cast<unsigned long long>(mid) << 32;
     if (n > want) lo = mid;
     else hi = mid - 1;
   }
@@ -808,14 +808,15 @@ __device__ __forceinline__ int warp_best(const unsigned long long* keys, int cou
 #pragma unroll
   for (int i = 0; i < R; ++i) key[i] = 32 * i + lane < count ? keys[32 * i + lane] : 0ull;
   __syncwarp();
-  const int m = warp_collect(key, warp_bound(key, W), lane, out);
+  const int m = warp_collect(key, warp_bound(key, W, W), lane, out);
   __syncwarp();
   return min(m, W);
 }
 
-// One block per row. A sieve first: the maxima are dealt to 256 groups, and the W-th largest of the groups' largest is
-// a bound that at least W maxima reach, and few more, as the best W sit in almost as many groups. What reaches it is
-// collected (about W + 2), and the best W of that are the row's picks.
+// One block per row. A sieve first: the maxima are dealt to 256 groups, and a value that W of the groups' largest
+// reach, or up to a quarter more (which ends the bisection early), is a bound that at least W maxima reach, and few
+// more, as the best W sit in almost as many groups. What reaches it is collected, and the best W of that are the row's
+// picks. The row is read 16 bytes a load (V = 128256, one row: 5.4 us, by words 7.5; 2048 rows: 54 and 60).
 // Where more than kPickSifted reach the bound (equal logits), every warp bisects over its share, 512 maxima at a
 // time together with what it kept before, and the best W of what the warps kept are the picks.
 // P.grouped: the last block to finish lays out the picks' rows: every pick that some row wants gets its place in
@@ -838,10 +839,18 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 5 : 1)
   const int n = (P.V + kHeadPick - 1) / kHeadPick;
   const float* mx = P.pick_max + static_cast<int64_t>(r) * P.picks;
   unsigned long long best = 0;
-#pragma unroll 8
-  for (int u = threadIdx.x; u < n; u += WARPS * 32) {
-    const unsigned long long x = make_key(mx[u], static_cast<uint32_t>(u));
-    best = x > best ? x : best;
+  const float4* mx4 = reinterpret_cast<const float4*>(mx);  // P.picks is a multiple of 4
+  const int n4 = (n + 3) / 4;
+#pragma unroll 4
+  for (int u4 = threadIdx.x; u4 < n4; u4 += WARPS * 32) {
+    const float4 x4 = mx4[u4];
+    const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int u = 4 * u4 + j;
+      const unsigned long long x = u < n ? make_key(xs[j], static_cast<uint32_t>(u)) : 0ull;
+      best = x > best ? x : best;
+    }
   }
   constexpr int lanes = WARPS * 32 / kPickGroups;  // of a group: neighbours
 #pragma unroll
@@ -859,17 +868,23 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 5 : 1)
 #pragma unroll
     for (int i = 0; i < kPickGroups / 32; ++i) groups += key[i] != 0 ? 1 : 0;
     groups = __reduce_add_sync(0xffffffffu, groups);
-    const unsigned long long bound = groups < W ? 1 : warp_bound(key, W);
+    const unsigned long long bound = groups < W ? 1 : warp_bound(key, W, W + W / 4);
     if (lane == 0) bound_s = bound;
   }
   __syncthreads();
   const unsigned long long bound = bound_s;
-#pragma unroll 8
-  for (int u = threadIdx.x; u < n; u += WARPS * 32) {
-    const unsigned long long x = make_key(mx[u], static_cast<uint32_t>(u));
-    if (x >= bound) {
-      const int at = atomicAdd(&sifted, 1);
-      if (at < kPickSifted) keys[at] = x;
+#pragma unroll 4
+  for (int u4 = threadIdx.x; u4 < n4; u4 += WARPS * 32) {
+    const float4 x4 = mx4[u4];
+    const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int u = 4 * u4 + j;
+      const unsigned long long x = make_key(xs[j], static_cast<uint32_t>(u));
+      if (x >= bound && u < n) {
+        const int at = atomicAdd(&sifted, 1);
+        if (at < kPickSifted) keys[at] = x;
+      }
     }
   }
   __syncthreads();
@@ -887,7 +902,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 5 : 1)
         key[j] = u < u1 ? make_key(mx[u], static_cast<uint32_t>(u)) : 0ull;
       }
       key[kPickHeld] = mine;
-      const int m = warp_collect(key, warp_bound(key, W), lane, kept);
+      const int m = warp_collect(key, warp_bound(key, W, W), lane, kept);
       __syncwarp();
       mine = lane < min(m, W) ? kept[lane] : 0ull;
       __syncwarp();
@@ -900,28 +915,50 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 5 : 1)
     const int m = count <= 64 ? warp_best<2>(keys, count, W, lane, keys)
                               : warp_best<kKeys / 32>(keys, count, W, lane, keys);
     const int unit = lane < m ? key_column(keys[lane]) : -1;
-    P.pick[static_cast<int64_t>(r) * 32 + lane] = unit;
     if (P.grouped) {
-      P.slot[static_cast<int64_t>(r) * 32 + lane] = unit >= 0 ? atomicAdd(P.count + unit, 1) : 0;
+      const int slot = unit >= 0 ? atomicAdd(P.count + unit, 1) : 0;
       __threadfence();
       __syncwarp();
       if (lane == 0) last = atomicAdd(P.done, 1) == static_cast<int>(gridDim.x) - 1;
+      P.slot[static_cast<int64_t>(r) * 32 + lane] = slot;
     }
+    P.pick[static_cast<int64_t>(r) * 32 + lane] = unit;
   }
   if (!P.grouped) return;
   __syncthreads();
   if (!last) return;
   __threadfence();
   constexpr int kAhead = 8;
-  for (int u0 = threadIdx.x; u0 < n; u0 += WARPS * 32 * kAhead) {
-    int c[kAhead];
+  for (int first = 0; first < n; first += WARPS * 32 * kAhead) {
+    const int u0 = first + threadIdx.x;
+    int c[kAhead], mine[2] = {0, 0};  // rows and items of the thread's picks, of which a warp takes its places at once
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) c[i] = u0 + WARPS * 32 * i < n ? __ldcg(P.count + u0 + WARPS * 32 * i) : 0;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
+      mine[0] += c[i];
+      mine[1] += (c[i] + kHeadDotRows - 1) / kHeadDotRows;
+    }
+    int to[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      int sum = mine[j];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      int before = 0;
+      if (lane == 31) before = atomicAdd(&placed[j], sum);
+      to[j] = __shfl_sync(0xffffffffu, before, 31) + sum - mine[j];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
       if (c[i] == 0) continue;
       const int u = u0 + WARPS * 32 * i, items = (c[i] + kHeadDotRows - 1) / kHeadDotRows;
-      const int at = atomicAdd(&placed[0], c[i]), it = atomicAdd(&placed[1], items);
+      const int at = to[0], it = to[1];
+      to[0] += c[i];
+      to[1] += items;
       P.base[u] = at;
       for (int k = 0; k < items; ++k)
         P.items[it + k] = make_int3(u, at + k * kHeadDotRows, min(kHeadDotRows, c[i] - k * kHeadDotRows));
@@ -1066,7 +1103,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
                    ? make_key(F.logits[(r * 32 + j) * kHeadPick + (lane & 15)], static_cast<uint32_t>(c))
                    : 0ull;
     }
-    const unsigned long long bound = warp_bound(key, 32);
+    const unsigned long long bound = warp_bound(key, 32, 32);
     best[lane] = 0;
     __syncwarp();
     warp_collect(key, bound, lane, best);
