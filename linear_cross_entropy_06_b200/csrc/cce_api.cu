@@ -314,7 +314,7 @@ LogprobWs carve_logprob(const cce_problem* p, int K, size_t off, void* base) {
   w.prep.lse = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.row_scale = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.tok = reinterpret_cast<int*>(take(sizeof(int) * n * k));
-  w.prep.tok_g = reinterpret_cast<float*>(take(sizeof(float) * n * k));
+  w.prep.entry = reinterpret_cast<float*>(take(sizeof(float) * n * k));
   w.prep.targets = reinterpret_cast<int64_t*>(take(sizeof(int64_t) * n));
   w.prep.one = reinterpret_cast<float*>(take(sizeof(float)));
   w.prep.E_out = reinterpret_cast<__nv_bfloat16*>(take(2 * n * static_cast<size_t>(p->D)));
@@ -516,8 +516,9 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
     A.lp_coef = lw.prep.coef;
     A.lp_coef_log = lw.prep.coef_log;
     A.lp_tok = lw.prep.tok;
-    A.lp_tok_g = lw.prep.tok_g;
+    A.lp_entry = lw.prep.entry;
     A.lp_k = lp->K;
+    A.lp_kb_chunk = cce::logit_kb_chunk(D);
     A.lp_inv_t = 1.f / lp->temperature;
     A.lp_scale = lw.prep.row_scale;
   }

@@ -38,7 +38,7 @@
 // has no unfinished dependency, the queue always drains; and with no boundary between chunks the
 // machine has a single tail per backward instead of one per chunk and kernel.
 //
-// Design (B200): one CTA per SM, 7 warps, 224 KB of shared memory.
+// Design (B200): one CTA per SM, 7 warps (12 for log-probabilities), 224 KB of shared memory.
 //   warp 0      producer: per stage (at most 48 KB, 4 deep) either the E_b K-block of 64 and one
 //               64 x 64 C box per half of the quad, or one K-half of a gradient tile (16 KB bulk
 //               copy, or zeros for a skipped half) and the 64 x 256 operand slice (dE, dC).
@@ -47,6 +47,9 @@
 //               store / reduce-add (dC / dE), while the MMA fills the other TMEM buffer.
 //   warp 6      scheduler: claims and decodes items into an 8-deep shared ring, at most LOOKAHEAD
 //               items ahead of the producer.
+// For log-probabilities warps 4..11 write out, warp 2 schedules, and warp 3 stores the quads' halves and publishes
+// them: with K in parts the MMA runs ahead of the write-out by two parts, not by a whole quad, so nothing that can be
+// done beside it is left in the write-out's way.
 #include "cce_device.cuh"
 #include "cce_internal.h"
 
@@ -65,7 +68,20 @@ constexpr int TILE_BYTES = kGradTileBytes;
 constexpr int REGION_BYTES = TILE_BYTES;  // two G halves (quad) or 4 x 8 KB staging (dE / dC)
 constexpr int STG_WARP = 8192;
 constexpr int RING = 8;
-constexpr int NUM_THREADS = 224;
+// Write-out warps: the quads of log-probabilities hold 256 columns of a row in registers while K is summed in parts, so
+// two warps share a row there (see logprob_quad). They are two warpgroups of their own then, to which the first one
+// (producer, MMA, scheduler, store) hands registers: 168 a thread at launch.
+template <bool LP>
+constexpr int kWriters = LP ? 8 : 4;
+template <bool LP>
+constexpr int kFirstWriter = LP ? 4 : 2;
+template <bool LP>
+constexpr int kScheduler = LP ? 2 : 6;
+constexpr int kStore = 3;  // LP
+template <bool LP>
+constexpr int kThreads = LP ? 384 : 224;
+constexpr int REGS_FEW = 72, REGS_MANY = 216;
+static_assert(REGS_FEW * 128 + REGS_MANY * 256 <= 168 * 384, "setmaxnreg draws on the launch's registers");
 constexpr int TMEM_COLS = 512;
 
 enum Kind : int { kQuad = 0, kDE = 1, kDC = 2, kEnd = 3 };
@@ -118,8 +134,9 @@ __device__ __forceinline__ uint32_t idesc_quad(int nh) {
 constexpr uint32_t IDESC_DC = idesc_bf16(BN, SLICE, true, true);    // M = vocabulary (G^T, MN-major)
 constexpr uint32_t IDESC_DE = idesc_bf16(BM, SLICE, false, true);   // M = rows (G, K-major)
 
-// Consumers of one ring entry: producer lane, MMA lane, one lane per write-out warp.
-constexpr uint32_t kRingConsumers = 1 + 1 + 4;
+// Consumers of one ring entry: producer lane, MMA lane, one lane per write-out warp, LP's storing lane.
+template <bool LP>
+constexpr uint32_t kRingConsumers = 1 + 1 + kWriters<LP> + (LP ? 1 : 0);
 
 __device__ __forceinline__ uint32_t swz(int row, int chunk) {
   return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
@@ -233,12 +250,28 @@ __device__ __forceinline__ void decode_item(int w, int g, int g_begin, int nchun
   }
 }
 
+// 64 columns of 32 rows of an accumulator, as they are or added to those of the parts before.
+__device__ __forceinline__ void add_part(uint32_t src, float (&z)[64], bool first) {
+  if (first) {
+    float(&lo)[32] = *reinterpret_cast<float(*)[32]>(z), (&hi)[32] = *reinterpret_cast<float(*)[32]>(z + 32);
+    tmem_ld64(src, lo, hi);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 64; c += 32) {
+    float v[32];
+    tmem_ld32(src + static_cast<uint32_t>(c), v);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      unpack2(add2(pack2(z[c + i], z[c + i + 1]), pack2(v[i], v[i + 1])), z[c + i], z[c + i + 1]);
+  }
+}
+
 // LP: the quads form the gradient of log-probabilities and entropy (see LogprobPrep) instead of the loss's:
-// G = p (coef + coef_log ln p) + sum_k tok_g[k] [v = t_k], p = exp(S / T - LSE), in fp32, rounded to bf16
-// once: the tokens' terms are added before the rounding, so that g (1 - p) of a confident token keeps its
-// leading bits.
+// G = p (coef + coef_log ln p), p = exp(S / T - LSE), in fp32, rounded to bf16 once, and at a given token the entry
+// that logprob_prep_kernel has formed from its log-probability.
 template <bool LP>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(kThreads<LP>, 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tmE128, const __grid_constant__ CUtensorMap tmC128,
                const __grid_constant__ CUtensorMap tmE64, const __grid_constant__ CUtensorMap tmC64,
                const __grid_constant__ CUtensorMap tmdC, const __grid_constant__ CUtensorMap tmdE,
@@ -263,14 +296,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(bar(kAccFull + a), 1);
-      mbar_init(bar(kAccEmpty + a), 128);
+      mbar_init(bar(kAccEmpty + a), 32 * kWriters<LP>);
     }
     mbar_init(bar(kDrain), 1);
-    mbar_init(bar(kRegion), 4);
-    mbar_init(bar(kGReady), 128);
+    mbar_init(bar(kRegion), kWriters<LP> + (LP ? 1 : 0));
+    mbar_init(bar(kGReady), 32 * kWriters<LP>);
     for (int i = 0; i < RING; ++i) {
       mbar_init(bar(kItemFull + i), 1);
-      mbar_init(bar(kItemEmpty + i), kRingConsumers);
+      mbar_init(bar(kItemEmpty + i), kRingConsumers<LP>);
       mbar_init(bar(kItemTaken + i), 1);
     }
     *abort_flag = 0;
@@ -289,207 +322,279 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int num_kb = (A.D + BK - 1) / BK;
   auto buffer = [&](int chunk) { return A.gscratch + static_cast<size_t>(chunk % kGradBuffers) * A.buf_bytes; };
 
-  if (warp == 6) {
-    // ---------------- scheduler ----------------
-    if (lane == 0) {
-      // A planning launch that gave up (its bounded barrier wait ran out; the error word is set)
-      // leaves the work lists unfinished: then no item is handed out at all.
-      const bool planned = ld_relaxed(A.err) == 0;
-      const int nchunks = planned ? *A.nchunks : 0;
-      const int total = planned ? A.grp_start[2 * nchunks] : 0;
-      int g = 0, g_begin = 0, g_end = A.grp_start[1];  // this CTA's claims only increase
-      for (uint32_t k = 0;; ++k) {
-        const int idx = static_cast<int>(k % RING);
-        if (!mbar_wait(bar(kItemEmpty + idx), ((k / RING) & 1u) ^ 1u, wc)) break;
-        if (k >= LOOKAHEAD) {
-          const uint32_t j = k - LOOKAHEAD;
-          if (!mbar_wait(bar(kItemTaken + j % RING), (j / RING) & 1u, wc)) break;
-        }
-        const int w = atomicAdd(A.qctr, 1);
-        WorkItem it;
-        if (w >= total) {
-          it.kind = kEnd;
-        } else {
-          while (w >= g_end) {
-            ++g;
-            g_begin = g_end;
-            g_end = A.grp_start[g + 1];
-          }
-          decode_item(w, g, g_begin, nchunks, A, it);
-        }
-        int4* dst = reinterpret_cast<int4*>(ring + idx);
-        const int4* src = reinterpret_cast<const int4*>(&it);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = src[i];
-        mbar_arrive(bar(kItemFull + idx));  // release: the entry is visible to the waiters
-        if (it.kind == kEnd) break;
-      }
+  const uint32_t reg0 = smem_u32(region);
+  // Stores the halves j0 and j0 + 1 of a quad from the region, each into its tile's slot.
+  auto bulk_store_halves = [&](const WorkItem& it, int j0) {
+    for (int jj = 0; jj < 2 && j0 + jj < it.s; ++jj) {
+      const int th = quad_half(it, j0 + jj);
+      uint8_t* dst = buffer(it.chunk) + static_cast<size_t>(quad_slot(it, j0 + jj)) * TILE_BYTES + (th & 1) * PART;
+      bulk_store(dst, reg0 + static_cast<uint32_t>(jj * PART), PART);
     }
-  } else if (warp == 0) {
-    // ---------------- producer ----------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued[STAGES] = {0, 0, 0, 0};
-      bool ok = true;
-      for (uint32_t k = 0; ok; ++k) {
-        const int idx = static_cast<int>(k % RING);
-        if (!mbar_wait(bar(kItemFull + idx), (k / RING) & 1u, wc)) break;
-        WorkItem it;
-        read_item(ring, idx, it);
-        mbar_arrive(bar(kItemEmpty + idx));
-        mbar_arrive(bar(kItemTaken + idx));
-        if (it.kind == kEnd) break;
-        if (it.kind == kQuad) {
-          if (it.s == 0) continue;  // no half: nothing to recompute
-          const int rb = it.key * BM;
-          const uint32_t stage_bytes = PART + static_cast<uint32_t>(it.s) * X_BOX;
-          for (int kb = 0; kb < num_kb; ++kb) {
-            if (!mbar_wait(bar(kEmpty + stage), phase ^ 1u, wc)) {
-              ok = false;
-              break;
+    bulk_commit_group();
+  };
+  // Publishes a quad's halves, once stored, to the dE / dC items that wait for them.
+  auto publish = [&](const WorkItem& it) {
+    bulk_wait_group0();
+    fence_proxy_async_global();
+    red_release_add(A.counters + A.ctr_g_b + it.chunk * A.nb + it.key, it.s);
+    for (int j = 0; j < it.s; ++j) red_release_add(A.counters + A.ctr_g_t + (quad_half(it, j) >> 1), 1);
+  };
+  const bool writer = warp >= kFirstWriter<LP> && warp < kFirstWriter<LP> + kWriters<LP>;
+  if (!writer) {
+    if constexpr (LP) regs_dec<REGS_FEW>();
+    if (warp == kScheduler<LP>) {
+      // ---------------- scheduler ----------------
+      if (lane == 0) {
+        // A planning launch that gave up (its bounded barrier wait ran out; the error word is set)
+        // leaves the work lists unfinished: then no item is handed out at all.
+        const bool planned = ld_relaxed(A.err) == 0;
+        const int nchunks = planned ? *A.nchunks : 0;
+        const int total = planned ? A.grp_start[2 * nchunks] : 0;
+        int g = 0, g_begin = 0, g_end = A.grp_start[1];  // this CTA's claims only increase
+        for (uint32_t k = 0;; ++k) {
+          const int idx = static_cast<int>(k % RING);
+          if (!mbar_wait(bar(kItemEmpty + idx), ((k / RING) & 1u) ^ 1u, wc)) break;
+          if (k >= LOOKAHEAD) {
+            const uint32_t j = k - LOOKAHEAD;
+            if (!mbar_wait(bar(kItemTaken + j % RING), (j / RING) & 1u, wc)) break;
+          }
+          const int w = atomicAdd(A.qctr, 1);
+          WorkItem it;
+          if (w >= total) {
+            it.kind = kEnd;
+          } else {
+            while (w >= g_end) {
+              ++g;
+              g_begin = g_end;
+              g_end = A.grp_start[g + 1];
             }
-            const uint32_t dst = smem_u32(stages + stage * STAGE_BYTES);
-            mbar_arrive_expect_tx(bar(kFull + stage), stage_bytes);
-            tma_load_2d(dst, &tmE128, bar(kFull + stage), kb * BK, rb);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {  // the quad's halves' C rows, in order
-              if (j < it.s) {
-                const int th = quad_half(it, j);
-                const int vrow = (th >> 1) * BN + (th & 1) * kSubTile;
-                tma_load_2d(dst + PART + j * X_BOX, &tmC128, bar(kFull + stage), kb * BK, vrow);
+            decode_item(w, g, g_begin, nchunks, A, it);
+          }
+          int4* dst = reinterpret_cast<int4*>(ring + idx);
+          const int4* src = reinterpret_cast<const int4*>(&it);
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = src[i];
+          mbar_arrive(bar(kItemFull + idx));  // release: the entry is visible to the waiters
+          if (it.kind == kEnd) break;
+        }
+      }
+    } else if (warp == 0) {
+      // ---------------- producer ----------------
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t issued[STAGES] = {0, 0, 0, 0};
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+          const int idx = static_cast<int>(k % RING);
+          if (!mbar_wait(bar(kItemFull + idx), (k / RING) & 1u, wc)) break;
+          WorkItem it;
+          read_item(ring, idx, it);
+          mbar_arrive(bar(kItemEmpty + idx));
+          mbar_arrive(bar(kItemTaken + idx));
+          if (it.kind == kEnd) break;
+          if (it.kind == kQuad) {
+            if (it.s == 0) continue;  // no half: nothing to recompute
+            const int rb = it.key * BM;
+            const uint32_t stage_bytes = PART + static_cast<uint32_t>(it.s) * X_BOX;
+            for (int kb = 0; kb < num_kb; ++kb) {
+              if (!mbar_wait(bar(kEmpty + stage), phase ^ 1u, wc)) {
+                ok = false;
+                break;
+              }
+              const uint32_t dst = smem_u32(stages + stage * STAGE_BYTES);
+              mbar_arrive_expect_tx(bar(kFull + stage), stage_bytes);
+              tma_load_2d(dst, &tmE128, bar(kFull + stage), kb * BK, rb);
+  #pragma unroll
+              for (int j = 0; j < 4; ++j) {  // the quad's halves' C rows, in order
+                if (j < it.s) {
+                  const int th = quad_half(it, j);
+                  const int vrow = (th >> 1) * BN + (th & 1) * kSubTile;
+                  tma_load_2d(dst + PART + j * X_BOX, &tmC128, bar(kFull + stage), kb * BK, vrow);
+                }
+              }
+              ++issued[stage];
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
               }
             }
-            ++issued[stage];
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
+            continue;
+          }
+          // dE / dC: every gradient tile this item reads must be stored
+          if (it.begin < it.end && !wait_counter(A.counters + it.dep_idx, it.dep_val, wc)) break;
+          const bool de = it.kind == kDE;
+          const uint8_t* buf = buffer(it.chunk);
+          const int x0 = it.s * SLICE;
+          // (tile index of the other operand, slot in the chunk's buffer, kept halves of the tile)
+          auto entry = [&](int i) {
+            if (de) {
+              const int2 en = A.entries_b[i];
+              return make_int3(en.x, (en.y & kSlotMask) - it.slot0, en.y >> kSlotBits);
+            }
+            const int x = A.entries_t[i].x;
+            return make_int3(x >> 4, i - it.slot0, flag_halves(x & 15));
+          };
+          const uint8_t* zero = static_cast<const uint8_t*>(A.zero_half);
+          int3 os_next = it.begin < it.end ? entry(it.begin) : make_int3(0, 0, 0);
+          for (int i = it.begin; i < it.end && ok; ++i) {
+            const int3 os = os_next;
+            if (i + 1 < it.end) os_next = entry(i + 1);
+            const uint8_t* tile = buf + static_cast<size_t>(os.y) * TILE_BYTES;
+            for (int h = 0; h < 2; ++h) {  // K-halves: 64 vocabulary columns (dE) or 64 rows (dC)
+              if (de && !((os.z >> h) & 1)) continue;  // a skipped half adds nothing to dE
+              if (!mbar_wait(bar(kEmpty + stage), phase ^ 1u, wc)) {
+                ok = false;
+                break;
+              }
+              const uint32_t dst = smem_u32(stages + stage * STAGE_BYTES);
+              mbar_arrive_expect_tx(bar(kFull + stage), STAGE_BYTES);
+              if (de) {  // G block h: rows 0..127, vocabulary 64h .. 64h + 63 (K-major A)
+                bulk_load(dst, tile + h * PART, PART, bar(kFull + stage));
+              } else {   // rows 64h .. 64h + 63 of both 64-column blocks (MN-major A = G^T); zeros for a
+                         // skipped half
+                bulk_load(dst, (os.z & 1) ? tile + h * (PART / 2) : zero, PART / 2, bar(kFull + stage));
+                bulk_load(dst + PART / 2, (os.z & 2) ? tile + PART + h * (PART / 2) : zero, PART / 2,
+                          bar(kFull + stage));
+              }
+              const int y = os.x * BM + 64 * h;  // K rows of the operand: C_t rows (dE), E_b rows (dC)
+              if (A.slab3d) {
+                tma_load_3d(dst + PART, de ? &tmC64 : &tmE64, bar(kFull + stage), 0, y, x0 / 64);
+              } else {
+  #pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  tma_load_2d(dst + PART + c * X_BOX, de ? &tmC64 : &tmE64, bar(kFull + stage), x0 + 64 * c, y);
+              }
+              ++issued[stage];
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
             }
           }
-          continue;
         }
-        // dE / dC: every gradient tile this item reads must be stored
-        if (it.begin < it.end && !wait_counter(A.counters + it.dep_idx, it.dep_val, wc)) break;
-        const bool de = it.kind == kDE;
-        const uint8_t* buf = buffer(it.chunk);
-        const int x0 = it.s * SLICE;
-        // (tile index of the other operand, slot in the chunk's buffer, kept halves of the tile)
-        auto entry = [&](int i) {
-          if (de) {
-            const int2 en = A.entries_b[i];
-            return make_int3(en.x, (en.y & kSlotMask) - it.slot0, en.y >> kSlotBits);
-          }
-          const int x = A.entries_t[i].x;
-          return make_int3(x >> 4, i - it.slot0, flag_halves(x & 15));
-        };
-        const uint8_t* zero = static_cast<const uint8_t*>(A.zero_half);
-        int3 os_next = it.begin < it.end ? entry(it.begin) : make_int3(0, 0, 0);
-        for (int i = it.begin; i < it.end && ok; ++i) {
-          const int3 os = os_next;
-          if (i + 1 < it.end) os_next = entry(i + 1);
-          const uint8_t* tile = buf + static_cast<size_t>(os.y) * TILE_BYTES;
-          for (int h = 0; h < 2; ++h) {  // K-halves: 64 vocabulary columns (dE) or 64 rows (dC)
-            if (de && !((os.z >> h) & 1)) continue;  // a skipped half adds nothing to dE
-            if (!mbar_wait(bar(kEmpty + stage), phase ^ 1u, wc)) {
+        if (*abort_flag) {
+          for (int u = 0; u < STAGES; ++u)
+            if (issued[u]) mbar_wait_drain(bar(kFull + u), (issued[u] - 1u) & 1u, 200000000ull);
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------- MMA issuer ----------------
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        uint32_t acc_iter = 0;
+        bool ok = true, issued_any = false;
+        for (uint32_t k = 0; ok; ++k) {
+          const int idx = static_cast<int>(k % RING);
+          if (!mbar_wait(bar(kItemFull + idx), (k / RING) & 1u, wc)) break;
+          WorkItem it;
+          read_item(ring, idx, it);
+          mbar_arrive(bar(kItemEmpty + idx));
+          if (it.kind == kEnd) break;
+          const bool quad = it.kind == kQuad;
+          if (quad ? it.s == 0 : it.begin == it.end) continue;  // no MMA for this item
+          uint32_t d = 0;
+          // the next accumulator, once the write-out warps have read what it held
+          auto next_acc = [&]() {
+            const int a = acc_iter & 1;
+            if (!mbar_wait(bar(kAccEmpty + a), ((acc_iter >> 1) & 1u) ^ 1u, wc)) return false;
+            tc_fence_after();
+            d = tmem_base + static_cast<uint32_t>(a * 2 * BN);
+            return true;
+          };
+          if (!next_acc()) break;
+          const int nstage = quad ? num_kb : (it.kind == kDE ? it.slot1 : 2 * (it.end - it.begin));
+          const uint32_t idesc = quad ? idesc_quad(it.s) : (it.kind == kDE ? IDESC_DE : IDESC_DC);
+          int j0 = 0;  // first stage of the accumulator's sum
+          for (int j = 0; j < nstage; ++j) {
+            if (LP && quad && j == j0 + A.lp_kb_chunk) {  // a part of K is complete
+              tc_commit(bar(kAccFull + (acc_iter & 1)));
+              ++acc_iter;
+              j0 = j;
+              if (!next_acc()) {
+                ok = false;
+                break;
+              }
+            }
+            if (!mbar_wait(bar(kFull + stage), phase, wc)) {
               ok = false;
               break;
             }
-            const uint32_t dst = smem_u32(stages + stage * STAGE_BYTES);
-            mbar_arrive_expect_tx(bar(kFull + stage), STAGE_BYTES);
-            if (de) {  // G block h: rows 0..127, vocabulary 64h .. 64h + 63 (K-major A)
-              bulk_load(dst, tile + h * PART, PART, bar(kFull + stage));
-            } else {   // rows 64h .. 64h + 63 of both 64-column blocks (MN-major A = G^T); zeros for a
-                       // skipped half
-              bulk_load(dst, (os.z & 1) ? tile + h * (PART / 2) : zero, PART / 2, bar(kFull + stage));
-              bulk_load(dst + PART / 2, (os.z & 2) ? tile + PART + h * (PART / 2) : zero, PART / 2,
-                        bar(kFull + stage));
+            tc_fence_after();
+            const uint32_t s0 = smem_u32(stages + stage * STAGE_BYTES);
+  #pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {  // 16 of the stage's 64 K values per MMA
+              uint64_t adesc, bdesc;
+              if (quad) {  // A = E_b K-block, B = the quad's halves' C rows (64 per half, rows of 128 bytes)
+                adesc = sdesc_sw128(s0 + 32u * kk, 16, 1024);
+                bdesc = sdesc_sw128(s0 + PART + 32u * kk, 16, 1024);
+              } else {
+                adesc = it.kind == kDE ? sdesc_sw128(s0 + 32u * kk, 16, 1024)
+                                       : sdesc_sw128(s0 + 2048u * kk, PART / 2, 1024);
+                bdesc = sdesc_sw128(s0 + PART + 2048u * kk, X_BOX, 1024);
+              }
+              tc_mma_bf16(d, adesc, bdesc, idesc, ((j - j0) | kk) != 0 ? 1u : 0u);
             }
-            const int y = os.x * BM + 64 * h;  // K rows of the operand: C_t rows (dE), E_b rows (dC)
-            if (A.slab3d) {
-              tma_load_3d(dst + PART, de ? &tmC64 : &tmE64, bar(kFull + stage), 0, y, x0 / 64);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                tma_load_2d(dst + PART + c * X_BOX, de ? &tmC64 : &tmE64, bar(kFull + stage), x0 + 64 * c, y);
-            }
-            ++issued[stage];
+            issued_any = true;
+            tc_commit(bar(kEmpty + stage));
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1u;
             }
           }
+          if (!ok) break;
+          tc_commit(bar(kAccFull + (acc_iter & 1)));
+          ++acc_iter;
+        }
+        if (*abort_flag && issued_any) {
+          tc_commit(bar(kDrain));
+          mbar_wait_drain(bar(kDrain), 0, 200000000ull);
         }
       }
-      if (*abort_flag) {
-        for (int u = 0; u < STAGES; ++u)
-          if (issued[u]) mbar_wait_drain(bar(kFull + u), (issued[u] - 1u) & 1u, 200000000ull);
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t acc_iter = 0;
-      bool ok = true, issued_any = false;
-      for (uint32_t k = 0; ok; ++k) {
-        const int idx = static_cast<int>(k % RING);
-        if (!mbar_wait(bar(kItemFull + idx), (k / RING) & 1u, wc)) break;
-        WorkItem it;
-        read_item(ring, idx, it);
-        mbar_arrive(bar(kItemEmpty + idx));
-        if (it.kind == kEnd) break;
-        const bool quad = it.kind == kQuad;
-        if (quad ? it.s == 0 : it.begin == it.end) continue;  // no MMA for this item
-        const int a = acc_iter & 1;
-        if (!mbar_wait(bar(kAccEmpty + a), ((acc_iter >> 1) & 1u) ^ 1u, wc)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(a * 2 * BN);
-        const int nstage = quad ? num_kb : (it.kind == kDE ? it.slot1 : 2 * (it.end - it.begin));
-        const uint32_t idesc = quad ? idesc_quad(it.s) : (it.kind == kDE ? IDESC_DE : IDESC_DC);
-        for (int j = 0; j < nstage; ++j) {
-          if (!mbar_wait(bar(kFull + stage), phase, wc)) {
-            ok = false;
-            break;
+    } else if (LP && warp == kStore) {
+      // ---------------- store (log-probabilities) ----------------
+      if (lane == 0) {
+        uint32_t rphase = 0, gphase = 0;
+        bool region_shared = true, ok = true;
+        auto region_free = [&]() {  // called where the write-out warps call theirs, and waits as they do
+          bulk_wait_group_read0();
+          mbar_arrive(bar(kRegion));
+          return mbar_wait(bar(kRegion), rphase++ & 1u, wc);
+        };
+        for (uint32_t k = 0; ok; ++k) {
+          const int idx = static_cast<int>(k % RING);
+          if (!mbar_wait(bar(kItemFull + idx), (k / RING) & 1u, wc)) break;
+          WorkItem it;
+          read_item(ring, idx, it);
+          mbar_arrive(bar(kItemEmpty + idx));
+          if (it.kind == kEnd) break;
+          if (it.kind != kQuad) {
+            if (it.kind == kDE && it.begin == it.end) continue;
+            if (region_shared) ok = region_free();
+            region_shared = false;
+            continue;
           }
-          tc_fence_after();
-          const uint32_t s0 = smem_u32(stages + stage * STAGE_BYTES);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // 16 of the stage's 64 K values per MMA
-            uint64_t adesc, bdesc;
-            if (quad) {  // A = E_b K-block, B = the quad's halves' C rows (64 per half, rows of 128 bytes)
-              adesc = sdesc_sw128(s0 + 32u * kk, 16, 1024);
-              bdesc = sdesc_sw128(s0 + PART + 32u * kk, 16, 1024);
-            } else {
-              adesc = it.kind == kDE ? sdesc_sw128(s0 + 32u * kk, 16, 1024)
-                                     : sdesc_sw128(s0 + 2048u * kk, PART / 2, 1024);
-              bdesc = sdesc_sw128(s0 + PART + 2048u * kk, X_BOX, 1024);
-            }
-            tc_mma_bf16(d, adesc, bdesc, idesc, (j | kk) != 0 ? 1u : 0u);
+          region_shared = true;
+          for (int j0 = 0; j0 < it.s && ok; j0 += 2) {
+            ok = region_free() && mbar_wait(bar(kGReady), gphase++ & 1u, wc);
+            // the chunk's buffer must no longer be read by the dE / dC items of chunk - 2
+            if (ok && j0 == 0 && it.dep_idx >= 0) ok = wait_counter(A.counters + it.dep_idx, it.dep_val, wc);
+            if (ok) bulk_store_halves(it, j0);
           }
-          issued_any = true;
-          tc_commit(bar(kEmpty + stage));
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (ok) publish(it);
         }
-        if (!ok) break;
-        tc_commit(bar(kAccFull + a));
-        ++acc_iter;
-      }
-      if (*abort_flag && issued_any) {
-        tc_commit(bar(kDrain));
-        mbar_wait_drain(bar(kDrain), 0, 200000000ull);
+        bulk_wait_group0();
       }
     }
   } else {
     // ---------------- write-out ----------------
-    const int q = warp & 3;  // TMEM lane quarter of this warp (warps 2..5 -> 2, 3, 0, 1)
+    if constexpr (LP) regs_inc<REGS_MANY>();
+    const int q = warp & 3;  // TMEM lane quarter of this warp (warps 2..5 -> 2, 3, 0, 1; 4..11: 0 to 3 twice)
+    const int half = LP ? (warp - kFirstWriter<LP>) >> 2 : 0;  // LP: which half of each two of a quad it forms
     const int row = q * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-    const bool leader = (warp == 2 && lane == 0);
-    const uint32_t reg0 = smem_u32(region);
+    const bool leader = (warp == kFirstWriter<LP> && lane == 0);
     const uint32_t stg = reg0 + static_cast<uint32_t>(q * STG_WARP);
     uint32_t acc_iter = 0, rphase = 0, gphase = 0;
     uint32_t img = 0;  // which of the two 4 KB staging images of this warp comes next
@@ -511,6 +616,127 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ++rphase;
       return r;
     };
+    // The halves j0 and j0 + 1 of a quad are in the region.
+    auto store_halves = [&](const WorkItem& it, int j0) {
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kGReady));
+      if (!LP && warp == kFirstWriter<LP>) {
+        if (!warp_wait(bar(kGReady), gphase & 1u)) ok = false;
+        else if (leader) bulk_store_halves(it, j0);
+      }
+      ++gphase;
+    };
+    // The quad has been stored, or is being stored by warp 3: on to the next item.
+    auto end_quad = [&](const WorkItem& it) {
+      if (!LP && leader && ok) publish(it);
+      __syncwarp();
+      if (*abort_flag) ok = false;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      region_shared = true;
+    };
+    // A quad of log-probabilities. The logits have to be those of the forward, whose accumulators take 512 or 256
+    // values of K: a whole sum is 5e-5 low at D = 4096 and logits of 11, p against the forward's lse is then low by as
+    // much, and the ln p + H of a confident row keeps nothing. So the same parts are summed here, by instructions that
+    // add in the same order, and added in registers, rounded to nearest: 256 columns of 128 rows, a row shared by two
+    // warps, of which each takes every other half. The accumulators alternate by parts and are free again before G is
+    // formed.
+    auto logprob_quad = [&](const WorkItem& it, int r) {
+      const bool row_in = r < A.N;
+      const float log2_s = row_in ? A.lse[r] * kLog2e : INFINITY;
+      const float coef = row_in ? A.lp_coef[r] : 0.f;
+      const float coef_l2 = row_in ? A.lp_coef_log[r] * 0.6931471805599453f : 0.f;
+      const float to_l2 = A.lp_inv_t * kLog2e;
+      const float rscale = row_in ? A.lp_scale[r] : 0.f;
+      // The row's given tokens are met in ascending order, as in the forward: `id` is the next one, the row's
+      // `at_id`-th. A quad costs a count (before its tile is there) and a step for each token in it, not one for
+      // each of K at every 32 columns (513 x 1032 x 32003, K = 8, 20, 32: 213, 220, 230 us
+      // against 239, 308, 392). The quad's halves come in ascending order.
+      int id = kNoToken, at_id = 0;
+      if (row_in && it.s > 0) {
+        const int first = quad_half(it, 0) * kSubTile;
+#pragma unroll 4
+        for (int k = 0; k < A.lp_k; ++k) {
+          const int t = A.lp_tok[static_cast<int64_t>(k) * A.N + r];
+          at_id += t < first ? 1 : 0;
+          id = t < first ? id : min(id, t);
+        }
+      }
+      float z0[64], z1[64];  // the warp's halves of the quad: `half` and 2 + half
+      for (int k0 = 0; it.s > 0 && k0 < num_kb; k0 += A.lp_kb_chunk) {
+        const int a = acc_iter & 1;
+        if (!warp_wait(bar(kAccFull + a), (acc_iter >> 1) & 1u)) return false;
+        tc_fence_after();
+        const uint32_t src = tmem_base + lane_off + static_cast<uint32_t>(a * 2 * BN + half * kSubTile);
+        if (half < it.s) add_part(src, z0, k0 == 0);
+        if (2 + half < it.s) add_part(src + 2 * kSubTile, z1, k0 == 0);
+        tc_fence_before();
+        mbar_arrive(bar(kAccEmpty + a));
+        ++acc_iter;
+      }
+      const uint32_t blk = reg0 + static_cast<uint32_t>(half * PART);
+      const uint64_t scale2 = pack2(to_l2, to_l2), lse2 = pack2(-log2_s, -log2_s), coef2 = pack2(coef, coef),
+                     log2 = pack2(coef_l2, coef_l2);
+      // Rounds of up to two halves: the region holds two 64-column parts. G is formed in registers while the round
+      // before is still being stored.
+      for (int j0 = 0; j0 < it.s && ok; j0 += 2) {
+        uint32_t g16[32];
+        const bool mine = j0 + half < it.s;
+        const int vb = quad_half(it, j0 + half) * kSubTile;  // the half's first vocabulary column
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < kSubTile / 32; ++c) {
+            float v[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = z0[32 * c + e];
+            const int col0 = vb + c * 32;
+            if (A.bias != nullptr) add_bias32(v, A.bias, col0, A.V);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float a0, a1;  // log2 p; p = 0 far below -200
+              unpack2(fma2(pack2(v[e], v[e + 1]), scale2, lse2), a0, a1);
+              const uint64_t p2 = pack2(ex2(a0), ex2(a1));
+              unpack2(mul2(p2, fma2(pack2(fmaxf(a0, -200.f), fmaxf(a1, -200.f)), log2, coef2)), v[e], v[e + 1]);
+            }
+            while (__any_sync(0xffffffffu, id < col0 + 32)) {
+              const int at = id - col0;
+              const bool here = at >= 0 && at < 32;
+              const float entry = here ? A.lp_entry[static_cast<int64_t>(at_id) * A.N + r] : 0.f;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = here && e == at ? entry : v[e];
+              if (at < 32) {
+                ++at_id;
+                id = at_id < A.lp_k ? A.lp_tok[static_cast<int64_t>(at_id) * A.N + r] : kNoToken;
+              }
+            }
+            // a row that asks for nothing is 0 whatever its logits are (S comes from E as it is)
+            const int left = log2_s != INFINITY ? A.V - col0 : 0;
+            if (left < 32) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = e < left ? v[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) g16[16 * c + e / 2] = pack_bf16x2(v[e], v[e + 1]);
+            if (A.dbias != nullptr) {  // dbias += column sums of G (this warp's 32 rows), fp32
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= rscale;
+              const float cs = warp_column_sums32(v, lane);
+              if (col0 + lane < A.V && cs != 0.f) atomicAdd(A.dbias + col0 + lane, cs);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 64; ++e) z0[e] = z1[e];
+        if (!region_free()) return false;
+        if (mine) {
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch)
+            st_shared_v4(blk + swz(row, ch), g16[4 * ch], g16[4 * ch + 1], g16[4 * ch + 2], g16[4 * ch + 3]);
+        }
+        store_halves(it, j0);
+      }
+      end_quad(it);
+      return true;
+    };
     for (uint32_t k = 0; ok; ++k) {
       const int idx = static_cast<int>(k % RING);
       if (!warp_wait(bar(kItemFull + idx), (k / RING) & 1u)) break;
@@ -522,25 +748,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int a = acc_iter & 1;
 
       if (it.kind == kQuad) {
-        const int b = it.key;
-        const int r = b * BM + row;
-        const float lse_r = (r < A.N) ? A.lse[r] : (LP ? INFINITY : 0.f);
-        const float lse_l2 = lse_r * kLog2e;
-        const float lp_coef = (LP && r < A.N) ? A.lp_coef[r] : 0.f;
-        const float lp_log2 = (LP && r < A.N) ? A.lp_coef_log[r] * 0.6931471805599453f : 0.f;
-        const float lp_scale = LP ? A.lp_inv_t * kLog2e : 0.f;
-        // The row's given tokens are met in ascending order, as in the forward: `id` is the next one, the row's
-        // `at_id`-th. A quad costs a count (before its tile is there) and a step for each token in it, not one for
-        // each of K at every 32 columns (513 x 1032 x 32003, K = 8, 20, 32: 213, 220, 230 us
-        // against 239, 308, 392). The quad's halves come in ascending order.
-        int id = kNoToken, at_id = 0;
-        if (LP && r < A.N && it.s > 0) {
-          const int first = quad_half(it, 0) * kSubTile;
-#pragma unroll 4
-          for (int k = 0; k < A.lp_k; ++k) at_id += A.lp_tok[static_cast<int64_t>(k) * A.N + r] < first ? 1 : 0;
-          if (at_id < A.lp_k) id = A.lp_tok[static_cast<int64_t>(at_id) * A.N + r];
+        const int r = it.key * BM + row;
+        if constexpr (LP) {
+          if (!logprob_quad(it, r)) break;
+          continue;
         }
-        const float lp_rscale = (LP && r < A.N) ? A.lp_scale[r] : 0.f;
+        const float lse_r = (r < A.N) ? A.lse[r] : 0.f;
+        const float lse_l2 = lse_r * kLog2e;
         const float sc = (r < A.N) ? A.scale[r] : 0.f;
         const float sc_p = sc * fmaf(2.f * A.z_loss, lse_r, 1.f);  // softmax part: (1 + 2 zl LSE) p
         const float sc_y = sc * A.onehot_coef;                     // onehot part: (1 - ls) y
@@ -555,7 +769,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // the chunk's buffer must no longer be read by the dE / dC items of chunk - 2
         if (leader && it.dep_idx >= 0 && !wait_counter(A.counters + it.dep_idx, it.dep_val, wc)) ok = false;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        uint8_t* buf = buffer(it.chunk);
         // rounds of up to two halves: the region holds two 64-column parts
         for (int j0 = 0; j0 < it.s && ok; j0 += 2) {
           if (!region_free()) {
@@ -577,35 +790,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const int col0 = vb + c * 32;
               tmem_ld32(tmem_base + lane_off + static_cast<uint32_t>(a * 2 * BN + j * kSubTile + c * 32), v);
               if (A.bias != nullptr) add_bias32(v, A.bias, col0, A.V);
-              if constexpr (LP) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const float l2 = fmaf(v[e], lp_scale, -lse_l2);  // log2 p; p = 0 far below -200
-                  v[e] = exp2f(l2) * fmaf(lp_log2, fmaxf(l2, -200.f), lp_coef);
-                }
-                while (__any_sync(0xffffffffu, id < col0 + 32)) {
-                  const int at = id - col0;
-                  const float gk = at >= 0 && at < 32 ? A.lp_tok_g[static_cast<int64_t>(at_id) * A.N + r] : 0.f;
+              for (int e = 0; e < 32; ++e) v[e] = sc_p * exp2f(fmaf(v[e], kLog2e, -lse_l2));
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] += e == at ? gk : 0.f;
-                  if (at < 32) {
-                    ++at_id;
-                    id = at_id < A.lp_k ? A.lp_tok[static_cast<int64_t>(at_id) * A.N + r] : kNoToken;
-                  }
-                }
-                // a row that asks for nothing is 0 whatever its logits are (S comes from E as it is)
-                const int left = lse_r != INFINITY ? A.V - col0 : 0;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (e >= left) v[e] = 0.f;
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = sc_p * exp2f(fmaf(v[e], kLog2e, -lse_l2));
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  if (c * 32 + e == tcol) v[e] -= sc_y;
-                  if (col0 + e >= A.V) v[e] = 0.f;
-                }
+              for (int e = 0; e < 32; ++e) {
+                if (c * 32 + e == tcol) v[e] -= sc_y;
+                if (col0 + e >= A.V) v[e] = 0.f;
               }
 #pragma unroll
               for (int h = 0; h < 4; ++h) {
@@ -615,53 +805,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                              pack_bf16x2(v[8 * h + 6], v[8 * h + 7]));
               }
               if (A.dbias != nullptr) {  // dbias += column sums of G (this warp's 32 rows), fp32
-                if constexpr (LP) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] *= lp_rscale;
-                }
                 const float cs = warp_column_sums32(v, lane);
                 if (col0 + lane < A.V && cs != 0.f) atomicAdd(A.dbias + col0 + lane, cs);
               }
             }
           }
-          fence_proxy_async_smem();
-          mbar_arrive(bar(kGReady));
-          if (warp == 2) {
-            if (!warp_wait(bar(kGReady), gphase & 1u)) {
-              ok = false;
-            } else if (leader) {
-              for (int jj = 0; jj < 2 && j0 + jj < it.s; ++jj) {  // each half into its tile's slot
-                const int th = quad_half(it, j0 + jj);
-                uint8_t* dst = buf + static_cast<size_t>(quad_slot(it, j0 + jj)) * TILE_BYTES + (th & 1) * PART;
-                bulk_store(dst, reg0 + static_cast<uint32_t>(jj * PART), PART);
-              }
-              bulk_commit_group();
-            }
-          }
-          ++gphase;
+          store_halves(it, j0);
         }
         if (mma) {
           tc_fence_before();
           mbar_arrive(bar(kAccEmpty + a));
           ++acc_iter;
         }
-        // publish the quad's halves to the dE / dC items that wait for them
-        if (leader && ok) {
-          bulk_wait_group0();
-          fence_proxy_async_global();
-          red_release_add(A.counters + A.ctr_g_b + it.chunk * A.nb + b, it.s);
-          for (int j = 0; j < it.s; ++j) red_release_add(A.counters + A.ctr_g_t + (quad_half(it, j) >> 1), 1);
-        }
-        __syncwarp();
-        if (*abort_flag) ok = false;
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        region_shared = true;
+        end_quad(it);
         continue;
       }
 
       // dE / dC
       const bool de = it.kind == kDE;
       const bool has = it.begin < it.end;
+      if (LP && half != 0) {  // these are written out by the first four warps
+        if (has) {
+          if (!warp_wait(bar(kAccFull + a), (acc_iter >> 1) & 1u)) break;
+          mbar_arrive(bar(kAccEmpty + a));
+          ++acc_iter;
+        }
+        if (de && !has) continue;
+        if (region_shared && !region_free()) break;
+        region_shared = false;
+        continue;
+      }
       // dC: the onehot terms -scale_r (1 - ls) E_r of the rows r whose target tile here was skipped
       // and whose target falls in this warp's 32 rows of the tile, in list order. The first two such
       // entries have this item's 256 columns of E_r loaded by the whole warp at once (16 bytes per
@@ -673,7 +846,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float h_coef0 = 0.f, h_coef1 = 0.f;
       uint4 h_cols0 = make_uint4(0, 0, 0, 0), h_cols1 = make_uint4(0, 0, 0, 0);  // columns x_item + 8 lane
       int oh_rest = -1;  // warp-uniform: first list entry handled step by step, or -1
-      if (!de && it.oh_begin < it.oh_end) {
+      if (!LP && !de && it.oh_begin < it.oh_end) {  // (log-probabilities: the entries are in G)
         const int64_t base_v = static_cast<int64_t>(it.key) * BN + q * 32 + A.vocab_start;
         const int64_t col = x_item + 8 * lane;
         int held = 0;
@@ -758,9 +931,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           if (lane == owner) add_vals(u8, coef);
         };
-        if (h_owner0 >= 0) add_held(h_cols0, h_owner0, h_coef0);
-        if (h_owner1 >= 0) add_held(h_cols1, h_owner1, h_coef1);
-        if (oh_rest >= 0) {  // the rest of the list, each entry by its owner lane
+        if (!LP && h_owner0 >= 0) add_held(h_cols0, h_owner0, h_coef0);
+        if (!LP && h_owner1 >= 0) add_held(h_cols1, h_owner1, h_coef1);
+        if (!LP && oh_rest >= 0) {  // the rest of the list, each entry by its owner lane
           const int64_t my_v = static_cast<int64_t>(it.key) * BN + q * 32 + lane;
           for (int i = oh_rest; i < it.oh_end; ++i) {
             const int r = A.oh_rows[i];
@@ -773,7 +946,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             add_vals(u8, -A.scale[r] * A.onehot_coef);
           }
         }
-        if (!de && A.dc_add != nullptr) {  // the smoothing term, the same for every row of dC
+        if (!LP && !de && A.dc_add != nullptr) {  // the smoothing term, the same for every row of dC
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             if (x + e < A.D) v0[e] = fmaf(A.dc_coef, A.dc_add[x + e], v0[e]);
@@ -852,11 +1025,11 @@ cudaError_t launch_one(const BwdLaunch& L, bool after_kernel, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   if (after_kernel) {
-    e = launch_after_previous(kernel, dim3(L.num_sms), dim3(NUM_THREADS), SMEM_BYTES, s, L.tmE128, L.tmC128, L.tmE64,
+    e = launch_after_previous(kernel, dim3(L.num_sms), dim3(kThreads<LP>), SMEM_BYTES, s, L.tmE128, L.tmC128, L.tmE64,
                               L.tmC64, L.tmdC, L.tmdE, L.args);
     if (e != cudaSuccess) return e;
   } else {
-    kernel<<<L.num_sms, NUM_THREADS, SMEM_BYTES, s>>>(L.tmE128, L.tmC128, L.tmE64, L.tmC64, L.tmdC, L.tmdE, L.args);
+    kernel<<<L.num_sms, kThreads<LP>, SMEM_BYTES, s>>>(L.tmE128, L.tmC128, L.tmE64, L.tmC64, L.tmdC, L.tmdE, L.args);
   }
   note_launches(1);
   return cudaGetLastError();

@@ -748,36 +748,41 @@ __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid
   if (threadIdx.x < 32) {
     const float lse = P.lse_in[r];
     const bool fine = lse != -INFINITY;  // a NaN goes on as NaN
-    float sum = 0.f, lp = 0.f;
+    float g = 0.f, lp = 0.f;
     bool any = false;
     int tok = kNoToken;
     if (lane < P.K) {
       const int64_t id = P.tokens[static_cast<int64_t>(r) * P.K + lane];
       any = id != P.ignore_index && id >= 0 && id < P.V;
-      sum = any && fine && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + lane] : 0.f;
+      g = any && fine && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + lane] : 0.f;
       tok = any && fine ? static_cast<int>(id) : kNoToken;
       if (tok != kNoToken) lp = P.logprobs[static_cast<int64_t>(r) * P.K + lane];
     }
     any = __any_sync(0xffffffffu, any) && fine;
-    const float g = sum * P.inv_t;
-    sum = warp_sum(sum);
+    const float sum = warp_sum(g);
     const float h = any && P.g_entropy != nullptr ? P.g_entropy[r] : 0.f;
-    const float coef = any ? -P.inv_t * (h != 0.f ? fmaf(h, P.entropy[r], sum) : sum) : 0.f;
+    const float H = h != 0.f ? P.entropy[r] : 0.f;
+    const float coef = any ? -P.inv_t * fmaf(h, H, sum) : 0.f;
     const float coef_log = any ? -P.inv_t * h : 0.f;
-    // the token's entry of G, and the scale that makes it a power of two
-    const float size = fabsf(exp2f(lp * kLog2e) * fmaf(coef_log, fmaxf(lp, -140.f), coef) + g);
-    const float entry = __shfl_sync(0xffffffffu, size, 0);
-    const float s = P.K == 1 && entry > 1e-30f && entry < 1e30f
-                        ? __uint_as_float((__float_as_uint(entry) & 0x7fffffu) | 0x3f800000u)
-                        : 1.f;
-    int place = 0;  // of the lane's token among the row's, in ascending order
+    int place = 0;     // of the lane's token among the row's, in ascending order
+    float same = 0.f;  // gradients of this token, which may be given more than once
     for (int k = 0; k < P.K; ++k) {
       const int other = __shfl_sync(0xffffffffu, tok, k);
+      const float g_other = __shfl_sync(0xffffffffu, g, k);
       place += other < tok || (other == tok && k < lane) ? 1 : 0;
+      same += other == tok ? g_other : 0.f;
     }
+    // the token's entry of G, and the scale that makes it a power of two
+    const float p = expf(lp);
+    const float from_g = p > 0.5f ? fmaf(-expm1f(lp), sum, same - sum) : fmaf(-p, sum, same);
+    const float entry = P.inv_t * fmaf(-h * p, fmaxf(lp, -140.f) + H, from_g);
+    const float size = fabsf(__shfl_sync(0xffffffffu, entry, 0));
+    const float s = P.K == 1 && size > 1e-30f && size < 1e30f
+                        ? __uint_as_float((__float_as_uint(size) & 0x7fffffu) | 0x3f800000u)
+                        : 1.f;
     if (lane < P.K) {
       P.tok[static_cast<int64_t>(place) * P.N + r] = tok;
-      P.tok_g[static_cast<int64_t>(place) * P.N + r] = g / s;
+      P.entry[static_cast<int64_t>(place) * P.N + r] = entry / s;
     }
     if (lane == 0) {
       P.coef[r] = coef / s;

@@ -22,14 +22,6 @@ using cce::fail;
 
 // Largest width of 8-bit operands: 127 * 127 * D stays below 2^31.
 constexpr int64_t kInt8MaxD = 131072;
-// K-blocks (of 64 values) summed in one accumulator, see the head of cce_head.cu. Every part is read once from tensor
-// memory, which the tensor cores feel (2048 x 2048 x 128256: 785 us with parts of 512 values, 763 with 1024, 752 with
-// the whole sum), and its sum drifts with its length: error of the log-probabilities against 64 bits 2.5e-6, 5.2e-6
-// and 1.1e-5, where fp32 sums have 2.9e-6. Narrow operands, whose fp32 sums are closer, get parts of 256.
-constexpr int kChunkBlocks = 8;
-constexpr int kChunkBlocksNarrow = 4;
-constexpr int64_t kNarrow = 2048;  // widths below
-
 bool sizes_ok(int64_t N, int64_t D, int64_t V, bool int8, bool set_error) {
   auto bad = [&](const char* msg) {
     if (set_error) fail(CCE_ERR_INVALID_ARG, "%s", msg);
@@ -192,7 +184,7 @@ cce_status head_args(int64_t N, int64_t D, int64_t V, bool int8, const void* E, 
   A->V = static_cast<int>(V);
   const int per_block = int8 ? 128 : 64;  // values of a 128-byte K-block
   A->num_kb = static_cast<int>(ceil_div(D, per_block));
-  A->kb_chunk = int8 ? A->num_kb : D < kNarrow ? kChunkBlocksNarrow : kChunkBlocks;
+  A->kb_chunk = int8 ? A->num_kb : cce::logit_kb_chunk(D);
   A->e_rows = static_cast<int>(std::min<int64_t>(cce::kHeadBM, (N + 7) / 8 * 8));
   A->bias = static_cast<const __nv_bfloat16*>(bias);
   A->e_scale = e_scale;

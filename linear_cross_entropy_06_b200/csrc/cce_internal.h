@@ -17,6 +17,13 @@ constexpr int kFwdBN = 256;
 constexpr int kNoToken = 0x7fffffff;  // in lists of given tokens: none (behind every column)
 constexpr int kSubTile = 64;  // vocabulary width of one saved tile max (and of a skip-rule unit)
 
+// K-blocks (of 64 values) of a log-probability's logit summed in one accumulator, see the head of cce_head.cu; the
+// backward recomputes the logits in the same parts. Every part is read once from tensor
+// memory, which the tensor cores feel (2048 x 2048 x 128256: 785 us with parts of 512 values, 763 with 1024, 752 with
+// the whole sum), and its sum drifts with its length: error of the log-probabilities against 64 bits 2.5e-6, 5.2e-6
+// and 1.1e-5, where fp32 sums have 2.9e-6. Narrow operands, whose fp32 sums are closer, get parts of 256.
+inline int logit_kb_chunk(int64_t D) { return D < 2048 ? 4 : 8; }
+
 // Backward tile: 128 rows x 128 vocabulary columns (a gradient tile and the unit of the work lists),
 // made of two 64-column halves. The skip rule decides each half (128 rows x kSubTile columns) on its
 // own; a tile is listed when either half is kept, and only its kept halves are recomputed, stored and
@@ -198,8 +205,9 @@ struct BwdArgs {
   const float* lp_coef;
   const float* lp_coef_log;
   const int* lp_tok;      // [lp_k, N], each row's in ascending order, kNoToken for none
-  const float* lp_tok_g;  // [lp_k, N], in the same order
+  const float* lp_entry;  // [lp_k, N], in the same order: the token's entry of G
   int lp_k;
+  int lp_kb_chunk;        // K-blocks summed in one accumulator: logit_kb_chunk(D)
   float lp_inv_t;         // 1 / temperature
   const float* lp_scale;  // [N]: see LogprobPrep
   int de_split;           // dE items a row block, slice and chunk: each adds its share of the row block's tiles
@@ -325,12 +333,15 @@ cudaError_t launch_fill_zero(void* dst, int64_t bytes, cudaStream_t s);
 // What the backward of the log-probabilities needs before its plan (cce_bwd_plan.cu, one launch). With
 // y = z / T, lp_k = y_{t_k} - lse, p = softmax(y) and the gradients g_k of lp_k and h of the entropy H:
 //   dz_v = (1 / T) (sum_k g_k [v = t_k] - p_v (sum_k g_k + h H + h ln p_v)).
-// Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and tok_g = g_k / T for the tokens tok
-// (in ascending order; kNoToken, behind the others, for ignored ones), all divided by the row's scale s. A row that asks for nothing, or has no finite
-// logit, gets zeros and lse = +inf (G = 0).
+// Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and the whole entry dz_t of each given token t (tok, in
+// ascending order; kNoToken, behind the others, for ignored ones), all divided by the row's scale s. A row that asks
+// for nothing, or has no finite logit, gets zeros and lse = +inf (G = 0).
+// The entry is formed here, from lp_k: a confident token's g (1 - p), or the g_k - p sum g of a student near its
+// teacher, is a small difference, which p = exp(z / T - lse) has lost to the size of its parts. With p - 1 =
+// expm1(lp_k) it is (g_t - sum g) - (p - 1) sum g - h p (lp_k + H), and nothing cancels that was rounded before.
 // The scale: G goes through bf16, and with one token a row dE of a row is mostly that token's entry times
 // its row of C, so an error of that one entry is an error of the whole row. With s in [1, 2) the
-// significand of the entry, it becomes a power of two and is kept exactly: dE is multiplied by s at the
+// significand of the entry, it becomes a power of two, which bf16 holds exactly: dE is multiplied by s at the
 // end, in fp32, and dC is formed from rows s E, whose rounding to bf16 falls on every element for itself
 // (256 x 128 x 4096, against 64 bits: dE 1.64e-3 and dC 2.2e-3 off, 2.6e-3 and 2.5e-3 without; the exact
 // result rounded to bf16 is 1.65e-3 off). With several tokens s is 1: the other entries are rounded all the
@@ -351,7 +362,7 @@ struct LogprobPrep {
   float* coef_log;
   float* lse;
   int* tok;
-  float* tok_g;
+  float* entry;
   int64_t* targets;         // V for the other rows: scored, their target in no tile of C
   float* one;               // [1] 1.0: the scale of every row's gradient
   float* row_scale;         // [N]: s
