@@ -18,7 +18,7 @@
 
 namespace {
 
-constexpr int32_t kVersion = 600;  // 0.6.0: log-probabilities, top alternatives, 8-bit product
+constexpr int32_t kVersion = 610;  // 0.6.1: statistics passed from log-probabilities to their backward
 
 using cce::aligned16;
 using cce::align_up;
@@ -312,6 +312,8 @@ LogprobWs carve_logprob(const cce_problem* p, int K, size_t off, void* base) {
   w.prep.coef = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.coef_log = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.lse = reinterpret_cast<float*>(take(sizeof(float) * n));
+  w.prep.row_max = reinterpret_cast<float*>(take(sizeof(float) * n));
+  w.prep.row_log2 = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.row_scale = reinterpret_cast<float*>(take(sizeof(float) * n));
   w.prep.tok = reinterpret_cast<int*>(take(sizeof(int) * n * k));
   w.prep.entry = reinterpret_cast<float*>(take(sizeof(float) * n * k));
@@ -415,6 +417,7 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
       P.ignore_index = lp->ignore_index;
       P.inv_t = 1.f / lp->temperature;
       P.lse_in = lp->lse;
+      P.stats_in = lp->row_stats;
       P.entropy = lp->entropy;
       P.logprobs = lp->logprobs;
       P.g_logprobs = lp->g_logprobs;
@@ -513,6 +516,8 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   A.ctr_g_t = w.plan.nchunks * w.plan.nb;
   A.ctr_b_done = A.ctr_g_t + w.plan.nt;
   if (lp != nullptr) {
+    A.lp_max = lw.prep.row_max;
+    A.lp_log2 = lw.prep.row_log2;
     A.lp_coef = lw.prep.coef;
     A.lp_coef_log = lw.prep.coef_log;
     A.lp_tok = lw.prep.tok;

@@ -268,8 +268,8 @@ __device__ __forceinline__ void add_part(uint32_t src, float (&z)[64], bool firs
 }
 
 // LP: the quads form the gradient of log-probabilities and entropy (see LogprobPrep) instead of the loss's:
-// G = p (coef + coef_log ln p), p = exp(S / T - LSE), in fp32, rounded to bf16 once, and at a given token the entry
-// that logprob_prep_kernel has formed from its log-probability.
+// G = p (coef + coef_log ln p), p = exp((S - S_max) / T) / sum, in fp32, rounded to bf16 once, and at a given token the
+// entry that logprob_prep_kernel has formed from its log-probability.
 template <bool LP>
 __global__ void __launch_bounds__(kThreads<LP>, 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tmE128, const __grid_constant__ CUtensorMap tmC128,
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
     // formed.
     auto logprob_quad = [&](const WorkItem& it, int r) {
       const bool row_in = r < A.N;
-      const float log2_s = row_in ? A.lse[r] * kLog2e : INFINITY;
+      const float top = row_in ? A.lp_max[r] : 0.f, log2_s = row_in ? A.lp_log2[r] : INFINITY;
       const float coef = row_in ? A.lp_coef[r] : 0.f;
       const float coef_l2 = row_in ? A.lp_coef_log[r] * 0.6931471805599453f : 0.f;
       const float to_l2 = A.lp_inv_t * kLog2e;
@@ -674,8 +674,8 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
         ++acc_iter;
       }
       const uint32_t blk = reg0 + static_cast<uint32_t>(half * PART);
-      const uint64_t scale2 = pack2(to_l2, to_l2), lse2 = pack2(-log2_s, -log2_s), coef2 = pack2(coef, coef),
-                     log2 = pack2(coef_l2, coef_l2);
+      const uint64_t top2 = pack2(-top, -top), scale2 = pack2(to_l2, to_l2), sum2 = pack2(-log2_s, -log2_s),
+                     coef2 = pack2(coef, coef), log2 = pack2(coef_l2, coef_l2);
       // Rounds of up to two halves: the region holds two 64-column parts. G is formed in registers while the round
       // before is still being stored.
       for (int j0 = 0; j0 < it.s && ok; j0 += 2) {
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               float a0, a1;  // log2 p; p = 0 far below -200
-              unpack2(fma2(pack2(v[e], v[e + 1]), scale2, lse2), a0, a1);
+              unpack2(fma2(add2(pack2(v[e], v[e + 1]), top2), scale2, sum2), a0, a1);
               const uint64_t p2 = pack2(ex2(a0), ex2(a1));
               unpack2(mul2(p2, fma2(pack2(fmaxf(a0, -200.f), fmaxf(a1, -200.f)), log2, coef2)), v[e], v[e + 1]);
             }

@@ -747,7 +747,10 @@ __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid
   }
   if (threadIdx.x < 32) {
     const float lse = P.lse_in[r];
-    const bool fine = lse != -INFINITY;  // a NaN goes on as NaN
+    const float top = P.stats_in != nullptr ? P.stats_in[r] : 0.f;
+    const float ln_s = P.stats_in != nullptr ? P.stats_in[static_cast<int64_t>(P.N) + r] : lse;
+    // every logit -inf, or not; a NaN goes on as NaN
+    const bool fine = P.stats_in != nullptr ? top != -INFINITY || ln_s != ln_s : lse != -INFINITY;
     float g = 0.f, lp = 0.f;
     bool any = false;
     int tok = kNoToken;
@@ -790,6 +793,8 @@ __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid
       P.row_scale[r] = s;
       scale_s = any ? s : 0.f;
       P.lse[r] = any ? lse : INFINITY;
+      P.row_max[r] = any ? top : 0.f;
+      P.row_log2[r] = any ? ln_s * kLog2e : INFINITY;
       P.targets[r] = any ? P.V : P.masked_id;
       A.scale[r] = 1.f;
       if (r == 0) *P.one = 1.f;

@@ -1027,6 +1027,10 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
       const float h = none || !any ? 0.f : ln_s - 0.6931471805599453f * (w / s);
       F.entropy[r] = failed ? nan : h;
       F.lse[r] = failed ? nan : (none ? -INFINITY : fmaf(m, F.inv_t, ln_s));
+      if (F.row_max != nullptr) {
+        F.row_max[r] = failed ? nan : m;
+        F.row_ln_s[r] = failed ? nan : ln_s;
+      }
     }
   }
   if (ROWS > 1 || F.top_k == 0) return;

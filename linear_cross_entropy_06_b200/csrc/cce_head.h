@@ -148,6 +148,8 @@ struct HeadFinish {
   float* logprobs;   // [N, K]
   float* entropy;    // [N]
   float* lse;        // [N]
+  float* row_max;    // [N] or null: largest logit, and ln of the sum of exp(y - y_max)
+  float* row_ln_s;
   float* top_logprobs;  // [N, top_k]
   int64_t* top_ids;
   int* err;

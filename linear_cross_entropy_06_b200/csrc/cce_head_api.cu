@@ -229,6 +229,14 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
                         const void* bias, const int64_t* tokens, float* logprobs, float* entropy, float* lse,
                         float* tile_max, float* top_logprobs, int64_t* top_ids, void* workspace, size_t workspace_bytes,
                         cce_stream_t stream) {
+  return cce_logprobs_stats(p, E, C, c_scale, bias, tokens, logprobs, entropy, lse, nullptr, tile_max, top_logprobs,
+                            top_ids, workspace, workspace_bytes, stream);
+}
+
+cce_status cce_logprobs_stats(const cce_logprob_problem* p, const void* E, const void* C, const float* c_scale,
+                              const void* bias, const int64_t* tokens, float* logprobs, float* entropy, float* lse,
+                              float* row_stats, float* tile_max, float* top_logprobs, int64_t* top_ids, void* workspace,
+                              size_t workspace_bytes, cce_stream_t stream) {
   cce::clear_last_error();
   if (!logprobs_ok(p, true)) return CCE_ERR_INVALID_ARG;
   const bool int8 = p->int8 != 0;
@@ -315,6 +323,8 @@ cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void*
     F.logprobs = K > 0 ? logprobs + r0 * K : nullptr;
     F.entropy = K > 0 ? entropy + r0 : nullptr;
     F.lse = K > 0 ? lse + r0 : nullptr;
+    F.row_max = K > 0 && row_stats != nullptr ? row_stats + r0 : nullptr;
+    F.row_ln_s = F.row_max != nullptr ? F.row_max + p->N : nullptr;
     F.top_logprobs = top_k > 0 ? top_logprobs + r0 * top_k : nullptr;
     F.top_ids = top_k > 0 ? top_ids + r0 * top_k : nullptr;
     F.err = A.err;
@@ -362,6 +372,17 @@ cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, co
                                  const float* grad_logprobs, const float* grad_entropy, float filter_eps, void* dE,
                                  void* dC, void* dbias, int32_t out_fp32, int64_t* filtered_tiles, void* workspace,
                                  size_t workspace_bytes, cce_stream_t stream) {
+  return cce_logprobs_stats_backward(p, E, C, bias, tokens, logprobs, lse, nullptr, entropy, tile_max, grad_logprobs,
+                                     grad_entropy, filter_eps, dE, dC, dbias, out_fp32, filtered_tiles, workspace,
+                                     workspace_bytes, stream);
+}
+
+cce_status cce_logprobs_stats_backward(const cce_logprob_problem* p, const void* E, const void* C, const void* bias,
+                                       const int64_t* tokens, const float* logprobs, const float* lse,
+                                       const float* row_stats, const float* entropy, const float* tile_max,
+                                       const float* grad_logprobs, const float* grad_entropy, float filter_eps,
+                                       void* dE, void* dC, void* dbias, int32_t out_fp32, int64_t* filtered_tiles,
+                                       void* workspace, size_t workspace_bytes, cce_stream_t stream) {
   cce::clear_last_error();
   if (!logprobs_ok(p, true)) return CCE_ERR_INVALID_ARG;
   if (p->int8 != 0) return fail(CCE_ERR_INVALID_ARG, "a classifier of 8-bit integers has no gradient");
@@ -385,6 +406,7 @@ cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, co
   g.K = p->num_tokens;
   g.temperature = p->temperature;
   g.lse = lse;
+  g.row_stats = row_stats;
   g.entropy = entropy;
   g.logprobs = logprobs;
   g.g_logprobs = grad_logprobs;

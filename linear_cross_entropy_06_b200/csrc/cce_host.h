@@ -47,6 +47,7 @@ struct LogprobGrads {
   int K;
   float temperature;
   const float* lse;           // [N] of the logits over the temperature
+  const float* row_stats;     // [2, N], see cce_logprobs_stats(), or null
   const float* entropy;       // [N]
   const float* logprobs;      // [N, K]
   const float* g_logprobs;    // [N, K] or null (zeros)

@@ -202,6 +202,8 @@ struct BwdArgs {
   uint64_t timeout_ns;
   int inject_stall;  // test hook: the first dE item waits for a count no item produces
   // Gradient of log-probabilities and entropy instead of the loss (lp_coef not null; see LogprobPrep)
+  const float* lp_max;    // ln p = (S - lp_max) / T - ln 2 lp_log2; lp_log2 +inf where a row asks for nothing
+  const float* lp_log2;
   const float* lp_coef;
   const float* lp_coef_log;
   const int* lp_tok;      // [lp_k, N], each row's in ascending order, kNoToken for none
@@ -335,10 +337,12 @@ cudaError_t launch_fill_zero(void* dst, int64_t bytes, cudaStream_t s);
 //   dz_v = (1 / T) (sum_k g_k [v = t_k] - p_v (sum_k g_k + h H + h ln p_v)).
 // Per row: coef = -(sum_k g_k + h H) / T, coef_log = -h / T, and the whole entry dz_t of each given token t (tok, in
 // ascending order; kNoToken, behind the others, for ignored ones), all divided by the row's scale s. A row that asks
-// for nothing, or has no finite logit, gets zeros and lse = +inf (G = 0).
+// for nothing, or has no finite logit, gets zeros and row_log2 = +inf (G = 0).
 // The entry is formed here, from lp_k: a confident token's g (1 - p), or the g_k - p sum g of a student near its
 // teacher, is a small difference, which p = exp(z / T - lse) has lost to the size of its parts. With p - 1 =
 // expm1(lp_k) it is (g_t - sum g) - (p - 1) sum g - h p (lp_k + H), and nothing cancels that was rounded before.
+// lse alone does not give p where it is large (at T = 2e-6 and logits of 8 its fp32 step is 0.25): ln p is formed as
+// (z - z_max) / T - ln S from the two numbers that the forward saves (row_stats).
 // The scale: G goes through bf16, and with one token a row dE of a row is mostly that token's entry times
 // its row of C, so an error of that one entry is an error of the whole row. With s in [1, 2) the
 // significand of the entry, it becomes a power of two, which bf16 holds exactly: dE is multiplied by s at the
@@ -352,6 +356,7 @@ struct LogprobPrep {
   int64_t ignore_index;
   float inv_t;
   const float* lse_in;
+  const float* stats_in;    // [2, N]: the rows' z_max and ln S, or null: then 0 and lse take their places
   const float* entropy;
   const float* logprobs;    // [N, K]
   const float* g_logprobs;  // [N, K] or null
@@ -360,7 +365,9 @@ struct LogprobPrep {
   int64_t masked_id;        // targets[r] of a row that asks for nothing
   float* coef;              // outputs
   float* coef_log;
-  float* lse;
+  float* lse;               // +inf for a row that asks for nothing
+  float* row_max;
+  float* row_log2;          // log2(e) ln S
   int* tok;
   float* entry;
   int64_t* targets;         // V for the other rows: scored, their target in no tile of C

@@ -101,6 +101,12 @@ def _check_tokens(tokens: torch.Tensor, N: int) -> int:
     return K
 
 
+def _check_stats(row_stats: Optional[torch.Tensor], N: int) -> None:
+    if row_stats is not None and (row_stats.dtype != torch.float32 or row_stats.shape != (2, N) or
+                                  not row_stats.is_contiguous()):
+        _refuse(f"row_stats must be contiguous float32 [2, {N}], got {row_stats.dtype} {tuple(row_stats.shape)}")
+
+
 def _aligned(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     """Contiguous, and at an address the kernels' 16-byte loads can start from (a slice of a larger
     buffer may begin anywhere: it is copied then)."""
@@ -133,18 +139,21 @@ def _on(dev: torch.device):
 
 def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor], top_k: int = 0,
                  bias: Optional[torch.Tensor] = None, temperature: float = 1.0, ignore_index: int = -100,
-                 save_max: bool = False, check: bool = False, save_lse: bool = True):
+                 save_max: bool = False, check: bool = False, save_lse: bool = True,
+                 row_stats: Optional[torch.Tensor] = None):
     """Run the forward for E [N, D] and tokens [N, K] (or None). Returns (logprobs [N, K], entropy [N],
     lse [N], tile_max or None, top_logprobs [N, top_k], top_ids [N, top_k]) as device tensors; the first
     three are None without tokens, the last two without alternatives. ``save_max`` keeps what a backward
-    that skips units needs; without ``save_lse`` lse is None."""
+    that skips units needs; without ``save_lse`` lse is None. ``row_stats``, fp32 [2, N], is filled with what the
+    backward forms probabilities from: with lse alone they carry its rounding, which tells at small temperatures."""
     lib = ops.load_library()
     N, D = _check_matrix(E)
     rows, scale = _check_classifier(C, D)
     V = rows.shape[0]
     _check_scalars(top_k, V, temperature)
     K = 0 if tokens is None else _check_tokens(tokens, N)
-    dev = _require_cuda(E, rows)
+    _check_stats(row_stats, N)
+    dev = _require_cuda(*(t for t in (E, rows, row_stats) if t is not None))
     E, rows = _aligned(E), _aligned(rows)
     if scale is not None:
         _require_cuda(E, scale)
@@ -174,9 +183,9 @@ def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor],
         top_lp = torch.empty(N, top_k, device=dev, dtype=torch.float32)
         top_ids = torch.empty(N, top_k, device=dev, dtype=torch.int64)
     with _on(dev):
-        _check(lib.cce_logprobs(p, E.data_ptr(), rows.data_ptr(), _ptr(scale), _ptr(bias), _ptr(tokens),
-                                _ptr(logprobs), _ptr(entropy), lse_ptr, _ptr(tile_max), _ptr(top_lp), _ptr(top_ids),
-                                ws.data_ptr(), ws_bytes, _stream(dev)))
+        _check(lib.cce_logprobs_stats(p, E.data_ptr(), rows.data_ptr(), _ptr(scale), _ptr(bias), _ptr(tokens),
+                                      _ptr(logprobs), _ptr(entropy), lse_ptr, _ptr(row_stats), _ptr(tile_max),
+                                      _ptr(top_lp), _ptr(top_ids), ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
     return logprobs, entropy, lse, tile_max, top_lp, top_ids
@@ -187,9 +196,9 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
                           grad_logprobs: Optional[torch.Tensor], grad_entropy: Optional[torch.Tensor],
                           filter_eps: float = 0.0, bias: Optional[torch.Tensor] = None, dbias: Optional[bool] = None,
                           temperature: float = 1.0, ignore_index: int = -100, out_fp32: int = ops.OUT_BF16,
-                          check: bool = False):
+                          check: bool = False, row_stats: Optional[torch.Tensor] = None):
     """Run the backward of ``cce_logprobs``. Returns (dE, dC, filtered_tiles) as device tensors, then
-    dbias when it is computed (by default whenever ``bias`` is given)."""
+    dbias when it is computed (by default whenever ``bias`` is given). ``row_stats`` as the forward filled it."""
     lib = ops.load_library()
     N, D = _check_matrix(E)
     if isinstance(C, Int8Rows):
@@ -202,6 +211,7 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
                        ("grad_logprobs", grad_logprobs, N * K), ("grad_entropy", grad_entropy, N)):
         if t is not None and (t.dtype != torch.float32 or t.numel() != n):
             _refuse(f"{name} must be float32 with {n} entries, got {t.dtype} {tuple(t.shape)}")
+    _check_stats(row_stats, N)
     if filter_eps > 0.0:
         need = -(-V // 64) * N
         if tile_max is None or tile_max.dtype != torch.float32 or tile_max.numel() < need:
@@ -209,8 +219,8 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     mode = int(out_fp32)
     if mode not in (ops.OUT_BF16, ops.OUT_FP32, ops.OUT_DE_FP32):
         _refuse(f"out_fp32 must be 0, 1 or 2, got {out_fp32!r}")
-    dev = _require_cuda(*(t for t in (E, rows, tokens, logprobs, lse, entropy, tile_max, grad_logprobs, grad_entropy)
-                          if t is not None))
+    dev = _require_cuda(*(t for t in (E, rows, tokens, logprobs, lse, row_stats, entropy, tile_max, grad_logprobs,
+                                      grad_entropy) if t is not None))
     E, rows, bias = _aligned(E), _aligned(rows), _aligned(_bias_arg(bias, V, dev))
     tokens, logprobs = tokens.contiguous(), logprobs.contiguous()
     lse, entropy = lse.contiguous(), entropy.contiguous()
@@ -230,10 +240,10 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     filtered = torch.empty(1, device=dev, dtype=torch.int64)
     ws = torch.empty(ws_bytes, device=dev, dtype=torch.uint8)
     with _on(dev):
-        _check(lib.cce_logprobs_backward(p, E.data_ptr(), rows.data_ptr(), _ptr(bias), tokens.data_ptr(),
-                                         logprobs.data_ptr(), lse.data_ptr(), entropy.data_ptr(), _ptr(tile_max),
-                                         _ptr(g_lp), _ptr(g_h), float(filter_eps), dE.data_ptr(), dC.data_ptr(),
-                                         _ptr(db), mode, filtered.data_ptr(), ws.data_ptr(), ws_bytes, _stream(dev)))
+        _check(lib.cce_logprobs_stats_backward(
+            p, E.data_ptr(), rows.data_ptr(), _ptr(bias), tokens.data_ptr(), logprobs.data_ptr(), lse.data_ptr(),
+            _ptr(row_stats), entropy.data_ptr(), _ptr(tile_max), _ptr(g_lp), _ptr(g_h), float(filter_eps),
+            dE.data_ptr(), dC.data_ptr(), _ptr(db), mode, filtered.data_ptr(), ws.data_ptr(), ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
     return (dE, dC, filtered) + ((db,) if want_dbias else ())
@@ -242,10 +252,11 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
 class _LinearLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, E, C, bias, tokens, shape, top_k, temperature, ignore_index, filter_eps):
+        stats = torch.empty(2, E.shape[0], device=E.device, dtype=torch.float32)
         logprobs, entropy, lse, tile_max, top_lp, top_ids = cce_logprobs(
-            E, C, tokens, top_k, bias, temperature, ignore_index, save_max=filter_eps > 0.0)
+            E, C, tokens, top_k, bias, temperature, ignore_index, save_max=filter_eps > 0.0, row_stats=stats)
         logprobs = logprobs.view(shape)  # here, where it adds no node to the graph
-        ctx.save_for_backward(E, C, bias, tokens, logprobs, lse, entropy, tile_max)
+        ctx.save_for_backward(E, C, bias, tokens, logprobs, lse, entropy, tile_max, stats)
         ctx.cfg = (temperature, ignore_index, filter_eps)
         ctx.set_materialize_grads(False)
         if top_k:
@@ -255,11 +266,11 @@ class _LinearLogprobs(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_logprobs, grad_entropy, _lp, _ids):
-        E, C, bias, tokens, logprobs, lse, entropy, tile_max = ctx.saved_tensors
+        E, C, bias, tokens, logprobs, lse, entropy, tile_max, stats = ctx.saved_tensors
         temperature, ignore_index, filter_eps = ctx.cfg
         want_db = bias is not None and ctx.needs_input_grad[2]
         out = cce_logprobs_backward(E, C, tokens, logprobs, lse, entropy, tile_max, grad_logprobs, grad_entropy,
-                                    filter_eps, bias, want_db, temperature, ignore_index)
+                                    filter_eps, bias, want_db, temperature, ignore_index, row_stats=stats)
         dbias = out[3].to(bias.dtype).reshape(bias.shape) if want_db else None
         return out[0], out[1], dbias, None, None, None, None, None, None
 

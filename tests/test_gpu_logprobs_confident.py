@@ -6,9 +6,9 @@ Tolerances, derived before the first run. dz: the error of one logit, 2^-14 sum 
 dy_v of the logits, |dy| <= dz / T, p_v is off by p_v (dy_v - sum_u p_u dy_u), at most 2 p_v (1 - p_v) dz / T, ln p_v by
 2 (1 - p_v) dz / T, and H by sum_u p_u |ln p_u + H| dz / T: all vanish as a row grows confident, as long as the
 backward's probabilities come from the logits that the statistics were formed of. What does not vanish is fp32 itself:
-the sum S, between 1 and 2 there, is added up in fewer than 32 steps of 2^-24 each, so p_v is off by 2^-19 p_v, ln p_v and H
-by 2^-18 (1 + |.|) with their own roundings. G is rounded to bf16 (2^-8 |G|; dC: its rows of E too), sums lose 2^-12 of the
-sum of magnitudes.
+the sum S, between 1 and 2 there, is added up in fewer than 32 steps of 2^-24 each, so p_v is off by 2^-19 p_v, ln p_v
+and H by 2^-18 (1 + |.|) with their own roundings. G is rounded to bf16 (2^-8 |G|; dC: its rows of E too), sums lose
+2^-12 of the sum of magnitudes.
 """
 import math
 
@@ -67,7 +67,7 @@ def check(got, ref, tol):
 @pytest.mark.parametrize("D", [520, 2048, 4096])
 @pytest.mark.parametrize("T", [1.0, 0.25])
 def test_gradients_of_confident_tokens(device, D, T):
-    """Even pairs of rows are given their best token, the others any: the best one's entry is then a probability only."""
+    """Half of the rows are given their best token, the others any: the best one's entry is then a probability only."""
     N = 160
     E, C, best, gen = confident(N, D, D, device)
     E = (E.double() * T).bfloat16()  # the same confidence at the temperature
