@@ -254,7 +254,9 @@ CCE_API cce_status cce_forward_noalloc(const cce_problem* p, const void* E, cons
  * With z = E C^T + bias, y = z / temperature, p = softmax(y), lse = ln sum_v exp(y_v), per row:
  *   log-probability of a given token t: y_t - lse;   entropy: lse - sum_v p_v y_v;
  *   alternatives: the top_k tokens with the largest y, highest first, the lower id first among equal
- *   ones, with y - lse. Close alternatives are ordered by their logits in 64 bits.
+ *   ones, with y - lse. Alternatives nearer to each other than the rounding of their 32-bit sums are
+ *   ordered by their logits in 64 bits (of candidates that 32-bit sums have chosen: eight more than top_k
+ *   groups of 16 columns, the best 32 of their logits).
  * A given token equal to ignore_index asks for nothing: its log-probability is 0; a row of which every
  * token is has entropy 0 and gradient 0, whatever stands in its row of E. A token outside [0, V) gives
  * NaN in its place, and CCE_ERR_TARGET_RANGE from cce_check_device_error(). A bias of -inf takes a
@@ -281,7 +283,7 @@ typedef struct {
 
 /* Bytes of device workspace cce_logprobs() needs (0 for a bad problem): 48 bytes a row and segment (a row
  * block's share of one SM, at most 148 / row blocks + 2 of them), 4 to 8 a row and given token, E in 8
- * bits with int8, and with alternatives V / 4 + 2700 bytes a row of at most 4096 rows (longer batches are
+ * bits with int8, and with alternatives V / 4 + 2944 bytes a row of at most 4096 rows (longer batches are
  * taken so many rows at a time): never anything of size N * V. */
 CCE_API size_t cce_logprobs_workspace_size(const cce_logprob_problem* p);
 

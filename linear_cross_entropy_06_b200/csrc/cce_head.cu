@@ -602,6 +602,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
+__device__ __forceinline__ float sum_squares(const uint4& u) {
+  const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float lo = __uint_as_float(us[k] << 16), hi = __uint_as_float(us[k] & 0xffff0000u);
+    s = fmaf(lo, lo, s);
+    s = fmaf(hi, hi, s);
+  }
+  return s;
+}
+
 __device__ __forceinline__ double warp_sum_f64(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -923,6 +935,18 @@ __global__ void __launch_bounds__(256) head_scatter_kernel(const __grid_constant
   if (u >= 0) P.rows[P.base[u] + P.slot[p]] = p;
 }
 
+constexpr int kDotStep = 64;  // bytes of a row a step
+// Steps of a warp summed in one accumulator: 128 values of bf16. What such a sum loses decides how many neighbours have
+// to be ordered in 64 bits (dot_error), and short ones cost nothing here.
+constexpr int kDotPart = 128 * 2 / kDotStep;
+
+// Bound on the error of a logit of head_dots_kernel (bf16), in units of |e| |c|, which bounds sum |e_d c_d|: an
+// instruction adds 16 products and the running sum, each cut at 2^-24 of the largest, 8 of them a part; the parts and
+// the warps' sums are added rounded to nearest, at most D / 512 + 10 additions.
+__device__ __forceinline__ float dot_error(int D) {
+  return (8.f * 17.f + 10.f + static_cast<float>(D) / 512.f) * 0x1p-24f;
+}
+
 // The row's softmax statistics from those of its segments: (m, s, w) and (m2, s2, w2) -> (m, s, w) of both.
 __device__ __forceinline__ void join_stats(float& m, float& s, float& w, float m2, float s2, float w2, float sc) {
   const float mn = fmaxf(m, m2);
@@ -942,7 +966,13 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float& w, float m
 // Alternatives: the best 32 of the picks' logits, sorted. They carry the rounding of 32-bit sums, so where two
 // neighbours are closer than that, their order (and which of them is the top_k-th) is not known yet: every run
 // of such neighbours is computed again in 64 bits, a warp for each logit, and ordered by that, the lower id first among
-// equal ones. Runs are short and rare (a few percent of the neighbours), so this reads little.
+// equal ones. What a sum loses grows with the magnitudes that it adds, not with what is left of them (two large
+// features of opposite sign, a bias that takes most of the product away), so the bound is on |e| |c|, and for 8 bits,
+// whose products are exact, on the product and the bias by themselves. Runs are short and few of the neighbours are in
+// one, so this reads little (the call with 20 alternatives against a bound of 2^-15 of the logit, which misses those
+// cases: 2048 x 2048 x 128256 987 us and 974, 1 x 4096 x 128256 198 and 191, 128 x 2048 x 128256 175 and 163).
+// What it cannot see: a token that nine or more others displace, all of which are below it by less than the rounding,
+// is not among the picks or the 32.
 template <int WARPS, int ROWS>
 __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __grid_constant__ HeadFinish F) {
   __shared__ float stats[WARPS][3];
@@ -1042,6 +1072,13 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
     return;
   }
 
+  float e_norm = 0.f;  // of the row of E, while the picks' logits are still being formed
+  if (wi == 0 && F.C8 == nullptr) {
+    const __nv_bfloat16* e = F.E + r * F.D;
+#pragma unroll 4
+    for (int d = lane * 8; d < F.D; d += 256) e_norm += sum_squares(ld_global_nc_v4(e + d));
+    e_norm = sqrtf(warp_sum(e_norm));
+  }
   wait_for_previous_grid();  // the picks' logits
   if (wi == 0) {
     unsigned long long key[kHeadPick];
@@ -1062,10 +1099,19 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) head_finish_kernel(const __
     const unsigned long long mine = warp_sort(best[lane], lane);
     best[lane] = mine;
     const float v = key_value(mine);
-    // Neighbours closer than what a 32-bit sum loses: the sums of 512 products carry up to a few 2^-24 of their
-    // largest part each (2^-15 of the logits leaves room); 8-bit products are exact but for three roundings.
-    const float scale = fmaxf(fabsf(__shfl_sync(0xffffffffu, v, 0)), fabsf(v));
-    const float tol = (F.C8 != nullptr ? 0x1p-21f : 0x1p-15f) * (scale < 3e38f ? scale : 0.f);
+    // What the two of a pair may be off: the sum of products, and the rounding of z (or for 8 bits, with |product| <=
+    // |z| + |bias|, three roundings of the product and that of z).
+    float off = 0x1p-24f * fabsf(v);
+    if (F.C8 != nullptr) {
+      const float b = F.bias != nullptr && mine != 0 ? fabsf(__bfloat162float(F.bias[key_column(mine)])) : 0.f;
+      off += 0x1.8p-23f * (fabsf(v) + b);
+    } else {
+      float c_norm = lane < F.wanted && F.pick[r * 32 + lane] >= 0 ? F.norm[r * 32 + lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c_norm = max_nan(c_norm, __shfl_xor_sync(0xffffffffu, c_norm, o));
+      off += dot_error(F.D) * 1.01f * e_norm * c_norm;
+    }
+    const float tol = off + __shfl_up_sync(0xffffffffu, off, 1);
     const float before = __shfl_up_sync(0xffffffffu, v, 1);
     const bool close = lane > 0 && mine != 0 && isfinite(v) && isfinite(before) && before - v <= tol;
     unsigned joins = __ballot_sync(0xffffffffu, close);  // bit i: i is close to i - 1
@@ -1135,13 +1181,10 @@ __device__ __forceinline__ void mma_16x8(int (&c)[4], uint32_t a0, uint32_t a1, 
 // positions are the same bytes of both operands, so nothing is rearranged.
 // Rows picked by index suit neither a TMA box nor an M = 128 tile (a pick has 7 rows of 2048 on average); the warp
 // instruction's 16-row tile wastes little, and the kernel is bound by reading C once.
-constexpr int kDotStep = 64;  // bytes of a row a step
-// Steps of a warp summed in one accumulator: 512 values (see the head of the file).
-constexpr int kDotPart = 512 * 2 / kDotStep;
-
+// sq (bf16): sums of squares of the pick's rows of C, from the same loads.
 template <bool I8, int WARPS, int TILES, int UNROLL, typename Acc>
 __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, const int* ids,
-                                         Acc* red, int64_t pitch, int lane, int w) {
+                                         Acc* red, float* sq, int64_t pitch, int lane, int w) {
   const int g = lane >> 2, t = lane & 3;
   const int steps = static_cast<int>((pitch + kDotStep - 1) / kDotStep);
   const char* er[TILES][2];
@@ -1155,6 +1198,7 @@ __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, co
   for (int nt = 0; nt < 2; ++nt)
     cr[nt] = static_cast<const char*>(P.C) + min(pick * kHeadPick + 8 * nt + g, P.V - 1) * pitch + t * 16;
   Acc sum[TILES][2][4] = {};
+  float squares[2] = {};
   for (int s0 = 0; s0 < steps; s0 += kDotPart * WARPS) {
     Acc acc[TILES][2][4] = {};
     const int s1 = min(steps, s0 + kDotPart * WARPS);
@@ -1171,6 +1215,12 @@ __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, co
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             a[u][mt][h] = in ? ld_global_nc_v4(er[mt][h] + off) : make_uint4(0, 0, 0, 0);
+      }
+      if (!I8) {
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) squares[nt] += sum_squares(b[u][nt]);
       }
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u)
@@ -1197,6 +1247,15 @@ __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, co
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         red[(16 * mt + g + 8 * (i >> 1)) * kHeadPick + 8 * nt + 2 * t + (i & 1)] = sum[mt][nt][i];
+  if (!I8) {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      float s = squares[nt];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if (t == 0) sq[8 * nt + g] = s;
+    }
+  }
 }
 
 // Ungrouped (ROWS = 16) every row has its own items.
@@ -1206,6 +1265,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   constexpr bool kGrouped = ROWS > 16;
   using Acc = typename std::conditional<I8, int, float>::type;
   __shared__ Acc red[WARPS][ROWS * kHeadPick];
+  __shared__ float sq[WARPS][kHeadPick];
   __shared__ int ids[kHeadDotRows];
   wait_for_previous_grid();
   let_next_grid_start();  // the head kernel has ended: the finish may join its statistics meanwhile
@@ -1219,8 +1279,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     if (threadIdx.x < item.z) ids[threadIdx.x] = kGrouped ? P.rows[item.y + threadIdx.x] : pair;
     __syncthreads();
     if (kGrouped || item.x >= 0) {
-      if (ROWS <= 16 || item.z <= 16) dot_item<I8, WARPS, 1, 4>(P, item.x, item.z, ids, red[w], pitch, lane, w);
-      else dot_item<I8, WARPS, ROWS / 16, 1>(P, item.x, item.z, ids, red[w], pitch, lane, w);
+      if (ROWS <= 16 || item.z <= 16) dot_item<I8, WARPS, 1, 4>(P, item.x, item.z, ids, red[w], sq[w], pitch, lane, w);
+      else dot_item<I8, WARPS, ROWS / 16, 1>(P, item.x, item.z, ids, red[w], sq[w], pitch, lane, w);
       __syncthreads();
       for (int i = threadIdx.x; i < item.z * kHeadPick; i += WARPS * 32) {
         Acc z = 0;
@@ -1232,6 +1292,15 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
           if (I8) v *= P.e_scale[p >> 5] * P.c_scale[col];
           if (P.bias != nullptr) v += __bfloat162float(P.bias[col]);
           P.logits[static_cast<int64_t>(p) * kHeadPick + i % kHeadPick] = v;
+        }
+        if (!I8) {  // the largest norm of the pick's rows of C, by the 16 threads of a row
+          float s = 0.f;
+#pragma unroll
+          for (int k = 0; k < WARPS; ++k) s += sq[k][i % kHeadPick];
+#pragma unroll
+          for (int o = kHeadPick / 2; o > 0; o >>= 1)
+            s = max_nan(s, __shfl_xor_sync(0xffffu << (lane & 16), s, o));
+          if (i % kHeadPick == 0) P.norm[p] = sqrtf(s);
         }
       }
     }

@@ -113,6 +113,7 @@ struct HeadPicks {
   int* rows;        // [32 N]: 32 row + j
   int3* items;      // [32 N]: pick, first of its rows, how many
   float* logits;    // [N, 32, 16]
+  float* norm;      // [N, 32]: largest norm of the pick's rows of C (bf16)
 };
 
 struct HeadMaps {
@@ -142,6 +143,7 @@ struct HeadFinish {
   const float* part_w;
   const int* pick;
   const float* logits;  // of the picks
+  const float* norm;    // HeadPicks.norm
   int wanted;
   int top_k;
   int after_dots;    // it follows head_dots_kernel, and may read what the head kernel wrote before that has ended

@@ -119,6 +119,7 @@ struct HeadWs {
   int* rows;
   int3* items;
   float* logits;
+  float* norm;
   int8_t* e8;      // [N, D]
   float* e_scale;  // [N]
   size_t bytes;
@@ -150,6 +151,7 @@ HeadWs carve(int64_t N, int64_t D, int64_t V, int K, int top_k, bool int8, bool 
     w.rows = reinterpret_cast<int*>(take(sizeof(int) * n * 32));
     w.items = reinterpret_cast<int3*>(take(sizeof(int3) * n * 32));
     w.logits = reinterpret_cast<float*>(take(sizeof(float) * n * 32 * cce::kHeadPick));
+    w.norm = reinterpret_cast<float*>(take(sizeof(float) * n * 32));
   }
   if (stats && N > 0) {
     // the largest of the slabs' splits: a slab with fewer row blocks has more segments a row block
@@ -318,6 +320,7 @@ cce_status cce_logprobs_stats(const cce_logprob_problem* p, const void* E, const
     F.part_w = w.part_w;
     F.pick = w.pick;
     F.logits = w.logits;
+    F.norm = w.norm;
     F.wanted = picks_wanted(top_k);
     F.top_k = top_k;
     F.logprobs = K > 0 ? logprobs + r0 * K : nullptr;
@@ -353,6 +356,7 @@ cce_status cce_logprobs_stats(const cce_logprob_problem* p, const void* E, const
     P.rows = w.rows;
     P.items = w.items;
     P.logits = w.logits;
+    P.norm = w.norm;
     CCE_TRY(cce::launch_head_picks(P, F, int8, sms, s));
   }
   return CCE_OK;

@@ -341,8 +341,9 @@ def linear_top_logprobs(e: torch.Tensor, c: Classifier, k: int, bias: Optional[t
     """The k (1 to 24) most probable tokens of each position under softmax((e @ c.T + bias) /
     temperature) and their log-probabilities, highest first, the lower id first among equal ones.
 
-    Close alternatives are ordered by their logits in 64 bits, so the ids depend neither on the batch
-    they are computed in nor on how the work was split. No gradient flows.
+    Alternatives nearer to each other than the rounding of their 32-bit sums are ordered by their logits in
+    64 bits, so the ids depend neither on the batch they are computed in nor on how the work was split,
+    unless nine or more tokens below one of them are as near to it as that. No gradient flows.
     """
     if k < 1:
         raise ValueError(f"k must be at least 1, got {k}")
