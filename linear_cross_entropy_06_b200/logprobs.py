@@ -11,7 +11,8 @@ z = e @ c.T + bias and y = z / temperature, and none but ``int8_linear`` writes 
 
 A classifier is a bf16 tensor [V, D], or ``Int8Rows`` (from ``quantize_int8``): its products then run on
 8-bit integers, the hidden states being rounded to 8 bits row by row inside the call, and no gradient
-flows. As in ``ops``, the compute runs in libcce.so on the current stream, arguments are checked here
+flows. ``linear_logprobs``, whose outputs do have gradients, therefore refuses an 8-bit classifier where one is
+asked for; the results of the others are never part of a graph. Forward-mode derivatives are refused. As in ``ops``, the compute runs in libcce.so on the current stream, arguments are checked here
 before a pointer reaches the library, and there is no CPU path.
 """
 from __future__ import annotations
@@ -21,6 +22,7 @@ import ctypes
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import ops
@@ -76,6 +78,14 @@ def _check_classifier(c: Classifier, D: int) -> Tuple[torch.Tensor, Optional[tor
     if rows.shape[1] != D:
         _refuse(f"c must be [V, {D}], got {tuple(rows.shape)}")
     return rows, scale
+
+
+def _no_tangent(name: str, e: torch.Tensor, c: Optional[Classifier] = None,
+                bias: Optional[torch.Tensor] = None) -> None:
+    """Refuse dual tensors: the outputs would come without a tangent, which torch takes as zero."""
+    for t in (e, bias) + (c if isinstance(c, Int8Rows) else (c,)):
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 def _flat(e: torch.Tensor) -> torch.Tensor:
@@ -295,6 +305,7 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
     as ``linear_top_logprobs`` does. ``shift`` makes e[..., i, :] predict tokens[..., i + 1] (one token a
     position); every output is then one position shorter along the sequence axis.
     """
+    _no_tangent("linear_logprobs", e, c, bias)
     lead = e.shape[:-1]
     if tokens.shape == lead:
         many = False
@@ -345,6 +356,7 @@ def linear_top_logprobs(e: torch.Tensor, c: Classifier, k: int, bias: Optional[t
     64 bits, so the ids depend neither on the batch they are computed in nor on how the work was split,
     unless nine or more tokens below one of them are as near to it as that. No gradient flows.
     """
+    _no_tangent("linear_top_logprobs", e, c, bias)
     if k < 1:
         raise ValueError(f"k must be at least 1, got {k}")
     out = cce_logprobs(_flat(e), c, None, k, bias, temperature)
@@ -358,6 +370,7 @@ def quantize_int8(x: torch.Tensor) -> Int8Rows:
     """Rows of x [rows, D] (bf16) as 8-bit integers with one scale each: scale = max |x| / 127 and
     values = x / scale, rounded to the nearest integer, halves to the even one. D must be a multiple of
     16. A row of zeros gets scale 0; a row that holds an infinity or a NaN gets the scale NaN."""
+    _no_tangent("quantize_int8", x)
     lib = ops.load_library()
     if x.dim() != 2 or x.dtype != torch.bfloat16:
         _refuse(f"x must be bfloat16 [rows, D], got {x.dtype} {tuple(x.shape)}")
@@ -378,6 +391,7 @@ def int8_linear(e: torch.Tensor, c: Int8Rows, bias: Optional[torch.Tensor] = Non
 
     Each row of e (bf16) is rounded to 8-bit integers with a scale of its own, the sums of integer
     products are exact, and the two scales and the bias are applied in fp32. No gradient flows."""
+    _no_tangent("int8_linear", e, c, bias)
     lib = ops.load_library()
     if not isinstance(c, Int8Rows):
         _refuse(f"c must be Int8Rows (see quantize_int8), got {type(c).__name__}")

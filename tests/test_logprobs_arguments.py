@@ -41,3 +41,26 @@ def test_the_calls_with_statistics_refuse_what_the_plain_ones_do(lib):
                                       size, None) == status
         assert lib.cce_logprobs_stats_backward(ctypes.byref(p), E, 16, None, 16, 16, 16, 16, 16, None, 16, 16, 0.0, 16,
                                                16, None, 0, 16, 16, size, None) == status
+
+
+def test_forward_mode_derivatives_are_refused(lib):
+    """A dual input has no requires_grad: without a refusal the outputs come back without a tangent."""
+    from torch.autograd import forward_ad
+
+    e, c = operands()
+    bias = torch.zeros(100)
+    q = lce.Int8Rows(torch.zeros(100, 32, dtype=torch.int8), torch.ones(100))
+    t = torch.zeros(4, dtype=torch.int64)
+    with forward_ad.dual_level():
+        de, dc, db = (forward_ad.make_dual(x, torch.ones_like(x)) for x in (e, c, bias))
+        dq = lce.Int8Rows(q.values, forward_ad.make_dual(q.scale, torch.ones(100)))
+        for call in (lambda: lce.linear_logprobs(de, c, t), lambda: lce.linear_logprobs(e, dc, t),
+                     lambda: lce.linear_logprobs(e, c, t, bias=db), lambda: lce.linear_logprobs(de, q, t, top_k=2),
+                     lambda: lce.linear_logprobs(e, dq, t), lambda: lce.linear_top_logprobs(de, c, 3),
+                     lambda: lce.linear_top_logprobs(e, q, 3, bias=db), lambda: lce.quantize_int8(dc),
+                     lambda: lce.int8_linear(de, q), lambda: lce.int8_linear(e, dq),
+                     lambda: lce.int8_linear(e, q, bias=db)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        with pytest.raises(lce.CCEError, match="no CPU path"):  # a level without dual inputs is nothing to refuse
+            lce.linear_logprobs(e, c, t, bias=bias)
