@@ -326,7 +326,7 @@ CCE_API cce_status cce_logprobs_backward(const cce_logprob_problem* p, const voi
  * largest logit z_max of each row, then the logarithm of the sum of exp((z - z_max) / temperature); lse =
  * z_max / temperature + that, rounded to fp32. The backward forms probabilities from row_stats where it is given. From
  * lse alone (NULL, and the plain calls) they carry its rounding, 2^-24 |lse|: 0.25 at a temperature of 2e-6 and
- * logits of 8.
+ * logits of 8. dbias_fp32 = 1 gives dbias in fp32 whatever out_fp32 says (the sums are fp32 in any case).
  */
 CCE_API cce_status cce_logprobs_stats(const cce_logprob_problem* p, const void* E, const void* C, const float* c_scale,
                                       const void* bias, const int64_t* tokens, float* logprobs, float* entropy,
@@ -337,8 +337,9 @@ CCE_API cce_status cce_logprobs_stats_backward(const cce_logprob_problem* p, con
                                                const float* lse, const float* row_stats, const float* entropy,
                                                const float* tile_max, const float* grad_logprobs,
                                                const float* grad_entropy, float filter_eps, void* dE, void* dC,
-                                               void* dbias, int32_t out_fp32, int64_t* filtered_tiles, void* workspace,
-                                               size_t workspace_bytes, cce_stream_t stream);
+                                               void* dbias, int32_t out_fp32, int32_t dbias_fp32,
+                                               int64_t* filtered_tiles, void* workspace, size_t workspace_bytes,
+                                               cce_stream_t stream);
 
 /* Rows of x (device bf16 [rows, D]) as 8-bit integers q [rows, D] and scales fp32 [rows]. A row of
  * zeros gets scale 0; a row with an infinity or a NaN gets the scale NaN. */

@@ -347,13 +347,14 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   const bool e32 = de_fp32(out_fp32), c32 = dc_fp32(out_fp32);
   const int64_t vs = p->vocab_start, vtot = vocab_total(p);
   float* dE_acc = e32 ? static_cast<float*>(dE) : w.dE_acc;
-  float* dbias_acc = dbias == nullptr ? nullptr : (c32 ? static_cast<float*>(dbias) : w.dbias_acc);
+  const bool b32 = c32 || (lp != nullptr && lp->dbias_fp32 != 0);
+  float* dbias_acc = dbias == nullptr ? nullptr : (b32 ? static_cast<float*>(dbias) : w.dbias_acc);
 
   // (the kernel that lays out a dense plan clears the header)
   if (N == 0 || lp == nullptr || filter_eps > 0.f) CCE_TRY(cudaMemsetAsync(w.hdr, 0, sizeof(WsHeader), s));
   if (N == 0) {  // no rows: dC = 0 (and dbias = 0)
     CCE_TRY(cce::launch_fill_zero(dC, V * D * (c32 ? 4 : 2), s));
-    if (dbias != nullptr) CCE_TRY(cce::launch_fill_zero(dbias, V * (c32 ? 4 : 2), s));
+    if (dbias != nullptr) CCE_TRY(cce::launch_fill_zero(dbias, V * (b32 ? 4 : 2), s));
     return cudaMemsetAsync(filtered_tiles, 0, sizeof(int64_t), s) == cudaSuccess ? CCE_OK
                                                                                   : fail(CCE_ERR_CUDA, "memset");
   }
@@ -568,7 +569,7 @@ cce_status backward_split(const cce_problem* p, const void* E, const void* C, co
   F.dC = dC;
   F.dc_bf16 = c32 ? 0 : 1;
   F.dbias_acc = dbias_acc;
-  F.dbias_out = (dbias != nullptr && !c32) ? dbias : nullptr;
+  F.dbias_out = (dbias != nullptr && !b32) ? dbias : nullptr;
   // (for log-probabilities without skipping there are none)
   const bool may_be_empty = lp == nullptr || filter_eps > 0.f;
   if (may_be_empty) CCE_TRY(cce::launch_empty_tiles(F, num_sms, !timed, s));

@@ -377,7 +377,7 @@ cce_status cce_logprobs_backward(const cce_logprob_problem* p, const void* E, co
                                  void* dC, void* dbias, int32_t out_fp32, int64_t* filtered_tiles, void* workspace,
                                  size_t workspace_bytes, cce_stream_t stream) {
   return cce_logprobs_stats_backward(p, E, C, bias, tokens, logprobs, lse, nullptr, entropy, tile_max, grad_logprobs,
-                                     grad_entropy, filter_eps, dE, dC, dbias, out_fp32, filtered_tiles, workspace,
+                                     grad_entropy, filter_eps, dE, dC, dbias, out_fp32, 0, filtered_tiles, workspace,
                                      workspace_bytes, stream);
 }
 
@@ -385,8 +385,9 @@ cce_status cce_logprobs_stats_backward(const cce_logprob_problem* p, const void*
                                        const int64_t* tokens, const float* logprobs, const float* lse,
                                        const float* row_stats, const float* entropy, const float* tile_max,
                                        const float* grad_logprobs, const float* grad_entropy, float filter_eps,
-                                       void* dE, void* dC, void* dbias, int32_t out_fp32, int64_t* filtered_tiles,
-                                       void* workspace, size_t workspace_bytes, cce_stream_t stream) {
+                                       void* dE, void* dC, void* dbias, int32_t out_fp32, int32_t dbias_fp32,
+                                       int64_t* filtered_tiles, void* workspace, size_t workspace_bytes,
+                                       cce_stream_t stream) {
   cce::clear_last_error();
   if (!logprobs_ok(p, true)) return CCE_ERR_INVALID_ARG;
   if (p->int8 != 0) return fail(CCE_ERR_INVALID_ARG, "a classifier of 8-bit integers has no gradient");
@@ -403,8 +404,10 @@ cce_status cce_logprobs_stats_backward(const cce_logprob_problem* p, const void*
   if (std::isnan(filter_eps)) return fail(CCE_ERR_INVALID_ARG, "filter_eps is NaN");
   if (out_fp32 < CCE_OUT_BF16 || out_fp32 > CCE_OUT_DE_FP32)
     return fail(CCE_ERR_INVALID_ARG, "out_fp32 must be CCE_OUT_BF16, CCE_OUT_FP32 or CCE_OUT_DE_FP32");
+  if (dbias_fp32 != 0 && dbias_fp32 != 1) return fail(CCE_ERR_INVALID_ARG, "dbias_fp32 must be 0 or 1");
   const cce_problem q = backward_problem(p);
   cce::LogprobGrads g{};
+  g.dbias_fp32 = dbias_fp32;
   g.tokens = tokens;
   g.ignore_index = p->ignore_index;
   g.K = p->num_tokens;

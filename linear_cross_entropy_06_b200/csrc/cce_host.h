@@ -52,6 +52,7 @@ struct LogprobGrads {
   const float* logprobs;      // [N, K]
   const float* g_logprobs;    // [N, K] or null (zeros)
   const float* g_entropy;     // [N] or null
+  int dbias_fp32;             // dbias in fp32 whatever the other outputs' type
 };
 size_t logprobs_backward_bytes(const cce_problem* p, int K, int32_t out_fp32);
 cce_status logprobs_backward(const cce_problem* p, const LogprobGrads& g, const void* E, const void* C,

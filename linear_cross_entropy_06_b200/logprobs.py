@@ -12,8 +12,9 @@ z = e @ c.T + bias and y = z / temperature, and none but ``int8_linear`` writes 
 A classifier is a bf16 tensor [V, D], or ``Int8Rows`` (from ``quantize_int8``): its products then run on
 8-bit integers, the hidden states being rounded to 8 bits row by row inside the call, and no gradient
 flows. ``linear_logprobs``, whose outputs do have gradients, therefore refuses an 8-bit classifier where one is
-asked for; the results of the others are never part of a graph. Forward-mode derivatives are refused. As in ``ops``, the compute runs in libcce.so on the current stream, arguments are checked here
-before a pointer reaches the library, and there is no CPU path.
+asked for; the results of the others are never part of a graph. Forward-mode derivatives are refused. As in
+``ops``, the compute runs in libcce.so on the current stream, arguments are checked here before a pointer
+reaches the library, and there is no CPU path.
 """
 from __future__ import annotations
 
@@ -206,9 +207,10 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
                           grad_logprobs: Optional[torch.Tensor], grad_entropy: Optional[torch.Tensor],
                           filter_eps: float = 0.0, bias: Optional[torch.Tensor] = None, dbias: Optional[bool] = None,
                           temperature: float = 1.0, ignore_index: int = -100, out_fp32: int = ops.OUT_BF16,
-                          check: bool = False, row_stats: Optional[torch.Tensor] = None):
+                          check: bool = False, row_stats: Optional[torch.Tensor] = None, dbias_fp32: bool = False):
     """Run the backward of ``cce_logprobs``. Returns (dE, dC, filtered_tiles) as device tensors, then
-    dbias when it is computed (by default whenever ``bias`` is given). ``row_stats`` as the forward filled it."""
+    dbias when it is computed (by default whenever ``bias`` is given), in fp32 with ``dbias_fp32``.
+    ``row_stats`` as the forward filled it."""
     lib = ops.load_library()
     N, D = _check_matrix(E)
     if isinstance(C, Int8Rows):
@@ -246,14 +248,15 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
     dc_dtype = torch.float32 if mode == ops.OUT_FP32 else torch.bfloat16
     dE = torch.empty(N, D, device=dev, dtype=de_dtype)
     dC = torch.empty(V, D, device=dev, dtype=dc_dtype)
-    db = torch.empty(V, device=dev, dtype=dc_dtype) if want_dbias else None
+    db = torch.empty(V, device=dev, dtype=torch.float32 if dbias_fp32 else dc_dtype) if want_dbias else None
     filtered = torch.empty(1, device=dev, dtype=torch.int64)
     ws = torch.empty(ws_bytes, device=dev, dtype=torch.uint8)
     with _on(dev):
         _check(lib.cce_logprobs_stats_backward(
             p, E.data_ptr(), rows.data_ptr(), _ptr(bias), tokens.data_ptr(), logprobs.data_ptr(), lse.data_ptr(),
             _ptr(row_stats), entropy.data_ptr(), _ptr(tile_max), _ptr(g_lp), _ptr(g_h), float(filter_eps),
-            dE.data_ptr(), dC.data_ptr(), _ptr(db), mode, filtered.data_ptr(), ws.data_ptr(), ws_bytes, _stream(dev)))
+            dE.data_ptr(), dC.data_ptr(), _ptr(db), mode, bool(dbias_fp32), filtered.data_ptr(), ws.data_ptr(),
+            ws_bytes, _stream(dev)))
         if check:
             _check(lib.cce_check_device_error(_ptr(ws), _stream(dev)))
     return (dE, dC, filtered) + ((db,) if want_dbias else ())
@@ -280,7 +283,8 @@ class _LinearLogprobs(torch.autograd.Function):
         temperature, ignore_index, filter_eps = ctx.cfg
         want_db = bias is not None and ctx.needs_input_grad[2]
         out = cce_logprobs_backward(E, C, tokens, logprobs, lse, entropy, tile_max, grad_logprobs, grad_entropy,
-                                    filter_eps, bias, want_db, temperature, ignore_index, row_stats=stats)
+                                    filter_eps, bias, want_db, temperature, ignore_index, row_stats=stats,
+                                    dbias_fp32=want_db and bias.dtype != torch.bfloat16)
         dbias = out[3].to(bias.dtype).reshape(bias.shape) if want_db else None
         return out[0], out[1], dbias, None, None, None, None, None, None
 
@@ -296,8 +300,9 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
     without a gradient; a position where every token does has entropy 0 and gives no gradient, whatever
     its hidden state holds. Other tokens outside [0, V) give NaN.
 
-    Gradients of both outputs flow to e, c and bias (policy gradients with an entropy bonus, preference
-    losses, distillation on a teacher's alternatives). They are exact by default; ``filter_eps`` > 0
+    Gradients of both outputs flow to e, c and bias, each in its own type (policy gradients with an
+    entropy bonus, preference losses, distillation on a teacher's alternatives). Nothing is left out of
+    them by default; ``filter_eps`` > 0
     skips units of 128 positions x 64 tokens whose probabilities are all below it, as
     ``linear_cross_entropy`` does, except units that hold a given token.
 

@@ -96,7 +96,7 @@ SIGNATURES = {
     "cce_logprobs_backward_workspace_size": (_SZ, [_LP, _I32]),
     "cce_logprobs_backward": (_I32, [_LP] + [_VP] * 10 + [_F32, _VP, _VP, _VP, _I32, _VP, _VP, _SZ, _VP]),
     "cce_logprobs_stats": (_I32, [_LP] + [_VP] * 13 + [_SZ, _VP]),
-    "cce_logprobs_stats_backward": (_I32, [_LP] + [_VP] * 11 + [_F32, _VP, _VP, _VP, _I32, _VP, _VP, _SZ, _VP]),
+    "cce_logprobs_stats_backward": (_I32, [_LP] + [_VP] * 11 + [_F32, _VP, _VP, _VP, _I32, _I32, _VP, _VP, _SZ, _VP]),
     "cce_quantize_int8": (_I32, [_VP, _I64, _I64, _VP, _VP, _VP]),
     "cce_int8_linear_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "cce_int8_linear": (_I32, [_I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP]),

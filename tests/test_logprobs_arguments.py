@@ -40,7 +40,9 @@ def test_the_calls_with_statistics_refuse_what_the_plain_ones_do(lib):
         assert lib.cce_logprobs_stats(ctypes.byref(p), E, 16, None, None, 16, 16, 16, 16, 16, None, None, None, 16,
                                       size, None) == status
         assert lib.cce_logprobs_stats_backward(ctypes.byref(p), E, 16, None, 16, 16, 16, 16, 16, None, 16, 16, 0.0, 16,
-                                               16, None, 0, 16, 16, size, None) == status
+                                               16, None, 0, 0, 16, 16, size, None) == status
+    assert lib.cce_logprobs_stats_backward(ctypes.byref(good), 16, 16, None, 16, 16, 16, 16, 16, None, 16, 16, 0.0, 16,
+                                           16, 16, 0, 2, 16, 16, 1 << 40, None) == 1  # dbias_fp32
 
 
 def test_forward_mode_derivatives_are_refused(lib):
