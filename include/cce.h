@@ -259,7 +259,8 @@ CCE_API cce_status cce_forward_noalloc(const cce_problem* p, const void* E, cons
  *   groups of 16 columns, the best 32 of their logits).
  * A given token equal to ignore_index asks for nothing: its log-probability is 0; a row of which every
  * token is has entropy 0 and gradient 0, whatever stands in its row of E. A token outside [0, V) gives
- * NaN in its place, and CCE_ERR_TARGET_RANGE from cce_check_device_error(). A bias of -inf takes a
+ * NaN in its place, no gradient, and CCE_ERR_TARGET_RANGE from cce_check_device_error(); the entropy of its row
+ * and that entropy's gradient are as usual. A bias of -inf takes a
  * column out of the softmax; a row of which nothing is left has log-probabilities -inf, entropy 0 and
  * gradient 0.
  *

@@ -756,9 +756,9 @@ __global__ void __launch_bounds__(kPrepThreads) logprob_prep_kernel(const __grid
     int tok = kNoToken;
     if (lane < P.K) {
       const int64_t id = P.tokens[static_cast<int64_t>(r) * P.K + lane];
-      any = id != P.ignore_index && id >= 0 && id < P.V;
-      g = any && fine && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + lane] : 0.f;
-      tok = any && fine ? static_cast<int>(id) : kNoToken;
+      any = id != P.ignore_index;  // a token out of range, too, asks for the entropy of its row
+      tok = any && fine && id >= 0 && id < P.V ? static_cast<int>(id) : kNoToken;
+      g = tok != kNoToken && P.g_logprobs != nullptr ? P.g_logprobs[static_cast<int64_t>(r) * P.K + lane] : 0.f;
       if (tok != kNoToken) lp = P.logprobs[static_cast<int64_t>(r) * P.K + lane];
     }
     any = __any_sync(0xffffffffu, any) && fine;

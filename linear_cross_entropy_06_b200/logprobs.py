@@ -298,13 +298,13 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
     optional [V]. tokens: int64, one a position in the shape e.shape[:-1], or up to 32 a position in the
     shape [..., K] (a token may be given twice). A token equal to ``ignore_index`` asks for nothing: 0,
     without a gradient; a position where every token does has entropy 0 and gives no gradient, whatever
-    its hidden state holds. Other tokens outside [0, V) give NaN.
+    its hidden state holds. Other tokens outside [0, V) give NaN
+    and no gradient; the entropy of their position is as usual.
 
     Gradients of both outputs flow to e, c and bias, each in its own type (policy gradients with an
     entropy bonus, preference losses, distillation on a teacher's alternatives). Nothing is left out of
-    them by default; ``filter_eps`` > 0
-    skips units of 128 positions x 64 tokens whose probabilities are all below it, as
-    ``linear_cross_entropy`` does, except units that hold a given token.
+    them by default; ``filter_eps`` > 0 skips units of 128 positions x 64 tokens whose probabilities are
+    all below it, as ``linear_cross_entropy`` does, except units that hold a given token.
 
     top_k: also return the top_k (up to 24) most probable tokens of each position, without gradients,
     as ``linear_top_logprobs`` does. ``shift`` makes e[..., i, :] predict tokens[..., i + 1] (one token a
