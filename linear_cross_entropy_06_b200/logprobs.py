@@ -84,6 +84,8 @@ def _check_classifier(c: Classifier, D: int) -> Tuple[torch.Tensor, Optional[tor
 def _no_tangent(name: str, e: torch.Tensor, c: Optional[Classifier] = None,
                 bias: Optional[torch.Tensor] = None) -> None:
     """Refuse dual tensors: the outputs would come without a tangent, which torch takes as zero."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # outside forward-mode there are none
+        return
     for t in (e, bias) + (c if isinstance(c, Int8Rows) else (c,)):
         if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
             raise NotImplementedError(f"{name} has no forward-mode derivative")
@@ -112,9 +114,8 @@ def _check_tokens(tokens: torch.Tensor, N: int) -> int:
     return K
 
 
-def _check_stats(row_stats: Optional[torch.Tensor], N: int) -> None:
-    if row_stats is not None and (row_stats.dtype != torch.float32 or row_stats.shape != (2, N) or
-                                  not row_stats.is_contiguous()):
+def _check_stats(row_stats: torch.Tensor, N: int) -> None:
+    if row_stats.dtype != torch.float32 or row_stats.shape != (2, N) or not row_stats.is_contiguous():
         _refuse(f"row_stats must be contiguous float32 [2, {N}], got {row_stats.dtype} {tuple(row_stats.shape)}")
 
 
@@ -163,8 +164,10 @@ def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor],
     V = rows.shape[0]
     _check_scalars(top_k, V, temperature)
     K = 0 if tokens is None else _check_tokens(tokens, N)
-    _check_stats(row_stats, N)
-    dev = _require_cuda(*(t for t in (E, rows, row_stats) if t is not None))
+    if row_stats is not None:
+        _check_stats(row_stats, N)
+        _require_cuda(E, row_stats)
+    dev = _require_cuda(E, rows)
     E, rows = _aligned(E), _aligned(rows)
     if scale is not None:
         _require_cuda(E, scale)
@@ -223,7 +226,8 @@ def cce_logprobs_backward(E: torch.Tensor, C: torch.Tensor, tokens: torch.Tensor
                        ("grad_logprobs", grad_logprobs, N * K), ("grad_entropy", grad_entropy, N)):
         if t is not None and (t.dtype != torch.float32 or t.numel() != n):
             _refuse(f"{name} must be float32 with {n} entries, got {t.dtype} {tuple(t.shape)}")
-    _check_stats(row_stats, N)
+    if row_stats is not None:
+        _check_stats(row_stats, N)
     if filter_eps > 0.0:
         need = -(-V // 64) * N
         if tile_max is None or tile_max.dtype != torch.float32 or tile_max.numel() < need:
