@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
@@ -323,6 +324,8 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
     else:
         raise ValueError(f"tokens shape {tuple(tokens.shape)} must equal e.shape[:-1] {tuple(lead)}, "
                          "with or without a last dimension of several tokens")
+    if math.isnan(filter_eps):
+        raise ValueError("filter_eps is NaN")
     if shift:
         if many or not lead or lead[-1] < 1:
             raise ValueError("shift needs one token a position and a sequence axis of length >= 1")
@@ -332,7 +335,7 @@ def linear_logprobs(e: torch.Tensor, c: Classifier, tokens: torch.Tensor, bias: 
     if not many:
         t = t.reshape(-1, 1)
     elif t.dim() != 2:
-        t = t.reshape(-1, t.shape[-1])
+        t = t.reshape(E.shape[0], t.shape[-1])
     grad = torch.is_grad_enabled() and (e.requires_grad or (bias is not None and bias.requires_grad) or
                                         (isinstance(c, torch.Tensor) and c.requires_grad))
     if not grad:

@@ -66,3 +66,11 @@ def test_forward_mode_derivatives_are_refused(lib):
                 call()
         with pytest.raises(lce.CCEError, match="no CPU path"):  # a level without dual inputs is nothing to refuse
             lce.linear_logprobs(e, c, t, bias=bias)
+
+
+def test_bad_arguments_are_named_where_they_are_given(lib):
+    e, c = operands()
+    with pytest.raises(lce.CCEError, match="1 to 32 tokens"):  # none, with more leading dimensions than one
+        lce.linear_logprobs(e.reshape(2, 2, 32), c, torch.zeros(2, 2, 0, dtype=torch.int64))
+    with pytest.raises(ValueError, match="filter_eps"):  # not first in the backward
+        lce.linear_logprobs(e, c, torch.zeros(4, dtype=torch.int64), filter_eps=float("nan"))
