@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
     // much, and the ln p + H of a confident row keeps nothing. So the same parts are summed here, by instructions that
     // add in the same order, and added in registers, rounded to nearest: 256 columns of 128 rows, a row shared by two
     // warps, of which each takes every other half. The accumulators alternate by parts and are free again before G is
-    // formed.
+    // formed. Against whole sums and four write-out warps: 4096 x 4096 x 128256 11.54 ms and 11.09, 2048 x 1024 x 50257
+    // 591 us and 613, 513 x 1032 x 32003 232 and 251. Reading a part takes the warps 900 cycles of its 4096.
     auto logprob_quad = [&](const WorkItem& it, int r) {
       const bool row_in = r < A.N;
       const float top = row_in ? A.lp_max[r] : 0.f, log2_s = row_in ? A.lp_log2[r] : INFINITY;

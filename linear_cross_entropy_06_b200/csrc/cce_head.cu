@@ -936,15 +936,12 @@ __global__ void __launch_bounds__(256) head_scatter_kernel(const __grid_constant
 }
 
 constexpr int kDotStep = 64;  // bytes of a row a step
-// Steps of a warp summed in one accumulator: 128 values of bf16. What such a sum loses decides how many neighbours have
-// to be ordered in 64 bits (dot_error), and short ones cost nothing here.
-constexpr int kDotPart = 128 * 2 / kDotStep;
 
 // Bound on the error of a logit of head_dots_kernel (bf16), in units of |e| |c|, which bounds sum |e_d c_d|: an
-// instruction adds 16 products and the running sum, each cut at 2^-24 of the largest, 8 of them a part; the parts and
-// the warps' sums are added rounded to nearest, at most D / 512 + 10 additions.
+// instruction adds 16 products and the running sum, each cut at 2^-24 of the largest, two of them a step; the steps and
+// the warps' sums are added rounded to nearest, at most D / 128 + 10 additions.
 __device__ __forceinline__ float dot_error(int D) {
-  return (8.f * 17.f + 10.f + static_cast<float>(D) / 512.f) * 0x1p-24f;
+  return (2.f * 17.f + 10.f + static_cast<float>(D) / 128.f) * 0x1p-24f;
 }
 
 // The row's softmax statistics from those of its segments: (m, s, w) and (m2, s2, w2) -> (m, s, w) of both.
@@ -970,7 +967,7 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float& w, float m
 // features of opposite sign, a bias that takes most of the product away), so the bound is on |e| |c|, and for 8 bits,
 // whose products are exact, on the product and the bias by themselves. Runs are short and few of the neighbours are in
 // one, so this reads little (the call with 20 alternatives against a bound of 2^-15 of the logit, which misses those
-// cases: 2048 x 2048 x 128256 987 us and 974, 1 x 4096 x 128256 198 and 191, 128 x 2048 x 128256 175 and 163).
+// cases: 2048 x 2048 x 128256 997 us and 981, 1 x 4096 x 128256 194 and 191, 128 x 2048 x 128256 171 and 163).
 // What it cannot see: a token that nine or more others displace, all of which are below it by less than the rounding,
 // is not among the picks or the 32.
 template <int WARPS, int ROWS>
@@ -1198,47 +1195,49 @@ __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, co
   for (int nt = 0; nt < 2; ++nt)
     cr[nt] = static_cast<const char*>(P.C) + min(pick * kHeadPick + 8 * nt + g, P.V - 1) * pitch + t * 16;
   Acc sum[TILES][2][4] = {};
-  float squares[2] = {};
-  for (int s0 = 0; s0 < steps; s0 += kDotPart * WARPS) {
-    Acc acc[TILES][2][4] = {};
-    const int s1 = min(steps, s0 + kDotPart * WARPS);
-    for (int s = s0 + w; s < s1; s += WARPS * UNROLL) {
-      uint4 b[UNROLL][2], a[UNROLL][TILES][2];
+  float squares[2][4] = {};
+#pragma unroll 1
+  for (int s = w; s < steps; s += WARPS * UNROLL) {
+    uint4 b[UNROLL][2], a[UNROLL][TILES][2];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int64_t off = static_cast<int64_t>(s + u * WARPS) * kDotStep;
-        const bool in = s + u * WARPS < s1 && off + t * 16 < pitch;
+    for (int u = 0; u < UNROLL; ++u) {
+      const int64_t off = static_cast<int64_t>(s + u * WARPS) * kDotStep;
+      const bool in = s + u * WARPS < steps && off + t * 16 < pitch;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) b[u][nt] = in ? ld_global_nc_v4(cr[nt] + off) : make_uint4(0, 0, 0, 0);
+      for (int nt = 0; nt < 2; ++nt) b[u][nt] = in ? ld_global_nc_v4(cr[nt] + off) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int mt = 0; mt < TILES; ++mt)
+      for (int mt = 0; mt < TILES; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            a[u][mt][h] = in ? ld_global_nc_v4(er[mt][h] + off) : make_uint4(0, 0, 0, 0);
-      }
-      if (!I8) {
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) squares[nt] += sum_squares(b[u][nt]);
-      }
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-        for (int mt = 0; mt < TILES; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const uint4 x = a[u][mt][0], y = a[u][mt][1];
-            mma_16x8(acc[mt][nt], x.x, y.x, x.y, y.y, b[u][nt].x, b[u][nt].y);
-            mma_16x8(acc[mt][nt], x.z, y.z, x.w, y.w, b[u][nt].z, b[u][nt].w);
-          }
+        for (int h = 0; h < 2; ++h)
+          a[u][mt][h] = in ? ld_global_nc_v4(er[mt][h] + off) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int mt = 0; mt < TILES; ++mt)
+    for (int u = 0; u < UNROLL; ++u) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[mt][nt][i] += acc[mt][nt][i];
+        for (int mt = 0; mt < TILES; ++mt) {
+          const uint4 x = a[u][mt][0], y = a[u][mt][1];
+          if constexpr (I8) {
+            mma_16x8(sum[mt][nt], x.x, y.x, x.y, y.y, b[u][nt].x, b[u][nt].y);
+            mma_16x8(sum[mt][nt], x.z, y.z, x.w, y.w, b[u][nt].z, b[u][nt].w);
+          } else {  // a step by itself, so that little is cut (dot_error)
+            float acc[4] = {};
+            mma_16x8(acc, x.x, y.x, x.y, y.y, b[u][nt].x, b[u][nt].y);
+            mma_16x8(acc, x.z, y.z, x.w, y.w, b[u][nt].z, b[u][nt].w);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+              unpack2(add2(pack2(sum[mt][nt][i], sum[mt][nt][i + 1]), pack2(acc[i], acc[i + 1])), sum[mt][nt][i],
+                      sum[mt][nt][i + 1]);
+          }
+        }
+        if constexpr (!I8) {  // the pick's rows by themselves: their squares are on the diagonal
+          const uint4 x = b[u][0], y = b[u][1];
+          mma_16x8(squares[nt], x.x, y.x, x.y, y.y, b[u][nt].x, b[u][nt].y);
+          mma_16x8(squares[nt], x.z, y.z, x.w, y.w, b[u][nt].z, b[u][nt].w);
+        }
+      }
+    }
   }
 #pragma unroll
   for (int mt = 0; mt < TILES; ++mt)
@@ -1247,14 +1246,9 @@ __device__ __forceinline__ void dot_item(const HeadPicks& P, int pick, int n, co
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         red[(16 * mt + g + 8 * (i >> 1)) * kHeadPick + 8 * nt + 2 * t + (i & 1)] = sum[mt][nt][i];
-  if (!I8) {
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      float s = squares[nt];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (t == 0) sq[8 * nt + g] = s;
-    }
+  if (!I8 && g >> 1 == t) {  // rows 8 nt + g, columns 8 nt + 2 t and the next
+    sq[g] = (g & 1) ? squares[0][1] : squares[0][0];
+    sq[8 + g] = (g & 1) ? squares[1][3] : squares[1][2];
   }
 }
 
