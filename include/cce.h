@@ -296,7 +296,8 @@ CCE_API size_t cce_logprobs_workspace_size(const cce_logprob_problem* p);
  *  logprobs device fp32 [N, num_tokens], entropy fp32 [N], lse fp32 [N] (num_tokens > 0)
  *  tile_max device fp32 [ceil(V / 64) * N] or NULL: saved for a backward with filter_eps > 0
  *  top_logprobs device fp32 [N, top_k], top_ids int64 [N, top_k] (top_k > 0)
- * After a device error (a bounded wait that ran out) every output is NaN, and every id -1.
+ * After a device error (a bounded wait that ran out) every output is NaN, and every id -1; with alternatives
+ * and more than 4096 rows, which are taken 4096 at a time, those of the rows before the failing ones stay.
  */
 CCE_API cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, const void* C, const float* c_scale,
                                 const void* bias, const int64_t* tokens, float* logprobs, float* entropy, float* lse,
@@ -304,7 +305,7 @@ CCE_API cce_status cce_logprobs(const cce_logprob_problem* p, const void* E, con
                                 size_t workspace_bytes, cce_stream_t stream);
 
 /* Bytes of device workspace cce_logprobs_backward() needs (0 for a bad problem): that of
- * cce_backward(), a copy of E, and 16 + 8 num_tokens bytes a row. */
+ * cce_backward(), a copy of E, and 32 + 8 num_tokens bytes a row. */
 CCE_API size_t cce_logprobs_backward_workspace_size(const cce_logprob_problem* p, int32_t out_fp32);
 
 /*
@@ -323,11 +324,12 @@ CCE_API cce_status cce_logprobs_backward(const cce_logprob_problem* p, const voi
                                          size_t workspace_bytes, cce_stream_t stream);
 
 /*
- * The two calls above with the rows' softmax statistics passed beside lse: row_stats, device fp32 [2, N] or NULL, the
- * largest logit z_max of each row, then the logarithm of the sum of exp((z - z_max) / temperature); lse =
- * z_max / temperature + that, rounded to fp32. The backward forms probabilities from row_stats where it is given. From
- * lse alone (NULL, and the plain calls) they carry its rounding, 2^-24 |lse|: 0.25 at a temperature of 2e-6 and
- * logits of 8. dbias_fp32 = 1 gives dbias in fp32 whatever out_fp32 says (the sums are fp32 in any case).
+ * The two calls above, with num_tokens > 0, and the rows' softmax statistics passed beside lse: row_stats, device
+ * fp32 [2, N] or NULL, the largest logit z_max of each row, then the logarithm of the sum of
+ * exp((z - z_max) / temperature); lse = z_max / temperature + that, rounded to fp32. The backward forms probabilities
+ * from row_stats where it is given. From lse alone (NULL, and the plain calls) they carry its rounding, 2^-24 |lse|:
+ * 0.25 at a temperature of 2e-6 and logits of 8. dbias_fp32 = 1 gives dbias in fp32 whatever out_fp32 says (the sums
+ * are fp32 in any case).
  */
 CCE_API cce_status cce_logprobs_stats(const cce_logprob_problem* p, const void* E, const void* C, const float* c_scale,
                                       const void* bias, const int64_t* tokens, float* logprobs, float* entropy,

@@ -650,8 +650,8 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
       const float rscale = row_in ? A.lp_scale[r] : 0.f;
       // The row's given tokens are met in ascending order, as in the forward: `id` is the next one, the row's
       // `at_id`-th. A quad costs a count (before its tile is there) and a step for each token in it, not one for
-      // each of K at every 32 columns (513 x 1032 x 32003, K = 8, 20, 32: 213, 220, 230 us
-      // against 239, 308, 392). The quad's halves come in ascending order.
+      // each of K at every 32 columns (513 x 1032 x 32003, K = 1, 8, 20, 32: 210, 212, 216, 222 us; looking for every
+      // token took 239, 308, 392 for the last three). The quad's halves come in ascending order.
       int id = kNoToken, at_id = 0;
       if (row_in && it.s > 0) {
         const int first = quad_half(it, 0) * kSubTile;

@@ -166,6 +166,8 @@ def cce_logprobs(E: torch.Tensor, C: Classifier, tokens: Optional[torch.Tensor],
     _check_scalars(top_k, V, temperature)
     K = 0 if tokens is None else _check_tokens(tokens, N)
     if row_stats is not None:
+        if not K:
+            _refuse("row_stats are formed with given tokens only")
         _check_stats(row_stats, N)
         _require_cuda(E, row_stats)
     dev = _require_cuda(E, rows)

@@ -29,6 +29,8 @@ def test_row_stats_are_checked(lib):
             L.cce_logprobs(e, c, t, row_stats=bad)
         with pytest.raises(lce.CCEError, match="row_stats"):
             L.cce_logprobs_backward(e, c, t, lp, lse, H, None, lp, H, row_stats=bad)
+    with pytest.raises(lce.CCEError, match="given tokens"):
+        L.cce_logprobs(e, c, None, 3, row_stats=torch.zeros(2, 4))
     with pytest.raises(lce.CCEError, match="no CPU path"):
         L.cce_logprobs(e, c, t, row_stats=torch.zeros(2, 4))
 
