@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
     // much, and the ln p + H of a confident row keeps nothing. So the same parts are summed here, by instructions that
     // add in the same order, and added in registers, rounded to nearest: 256 columns of 128 rows, a row shared by two
     // warps, of which each takes every other half. The accumulators alternate by parts and are free again before G is
-    // formed. Against whole sums and four write-out warps: 4096 x 4096 x 128256 11.54 ms and 11.09, 2048 x 1024 x 50257
-    // 591 us and 613, 513 x 1032 x 32003 232 and 251. Reading a part takes the warps 900 cycles of its 4096.
+    // formed. Against whole sums and four write-out warps: 4096 x 4096 x 128256 11.6 ms and 11.5, 2048 x 1024 x 50257
+    // 587 us and 652, 513 x 1032 x 32003 210 and 247. Reading a part takes the warps 900 cycles of its 4096.
     auto logprob_quad = [&](const WorkItem& it, int r) {
       const bool row_in = r < A.N;
       const float top = row_in ? A.lp_max[r] : 0.f, log2_s = row_in ? A.lp_log2[r] : INFINITY;
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
       const float rscale = row_in ? A.lp_scale[r] : 0.f;
       // The row's given tokens are met in ascending order, as in the forward: `id` is the next one, the row's
       // `at_id`-th. A quad costs a count (before its tile is there) and a step for each token in it, not one for
-      // each of K at every 32 columns (513 x 1032 x 32003, K = 1, 8, 20, 32: 210, 212, 216, 222 us; looking for every
+      // each of K at every 32 columns (513 x 1032 x 32003, K = 1, 8, 20, 32: 198, 202, 206, 210 us; looking for every
       // token took 239, 308, 392 for the last three). The quad's halves come in ascending order.
       int id = kNoToken, at_id = 0;
       if (row_in && it.s > 0) {
@@ -662,14 +662,19 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
           id = t < first ? id : min(id, t);
         }
       }
-      float z0[64], z1[64];  // the warp's halves of the quad: `half` and 2 + half
+      // The warp's halves of the quad, `half` and 2 + half; of one that the quad does not have, whatever the
+      // accumulator holds. Given a value here and in every part, the registers are free between the quads (where only
+      // a half that is there gives them one, they are kept, and spill: 2048 x 2048 x 128256 3.09 ms against 2.97).
+      float z0[64], z1[64];
+#pragma unroll
+      for (int e = 0; e < 64; ++e) z0[e] = z1[e] = 0.f;
       for (int k0 = 0; it.s > 0 && k0 < num_kb; k0 += A.lp_kb_chunk) {
         const int a = acc_iter & 1;
         if (!warp_wait(bar(kAccFull + a), (acc_iter >> 1) & 1u)) return false;
         tc_fence_after();
         const uint32_t src = tmem_base + lane_off + static_cast<uint32_t>(a * 2 * BN + half * kSubTile);
-        if (half < it.s) add_part(src, z0, k0 == 0);
-        if (2 + half < it.s) add_part(src + 2 * kSubTile, z1, k0 == 0);
+        add_part(src, z0, k0 == 0);
+        add_part(src + 2 * kSubTile, z1, k0 == 0);
         tc_fence_before();
         mbar_arrive(bar(kAccEmpty + a));
         ++acc_iter;
