@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
           }
           int4* dst = reinterpret_cast<int4*>(ring + idx);
           const int4* src = reinterpret_cast<const int4*>(&it);
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = src[i];
           mbar_arrive(bar(kItemFull + idx));  // release: the entry is visible to the waiters
           if (it.kind == kEnd) break;
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
               const uint32_t dst = smem_u32(stages + stage * STAGE_BYTES);
               mbar_arrive_expect_tx(bar(kFull + stage), stage_bytes);
               tma_load_2d(dst, &tmE128, bar(kFull + stage), kb * BK, rb);
-  #pragma unroll
+#pragma unroll
               for (int j = 0; j < 4; ++j) {  // the quad's halves' C rows, in order
                 if (j < it.s) {
                   const int th = quad_half(it, j);
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
               if (A.slab3d) {
                 tma_load_3d(dst + PART, de ? &tmC64 : &tmE64, bar(kFull + stage), 0, y, x0 / 64);
               } else {
-  #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 4; ++c)
                   tma_load_2d(dst + PART + c * X_BOX, de ? &tmC64 : &tmE64, bar(kFull + stage), x0 + 64 * c, y);
               }
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads<LP>, 1)
             }
             tc_fence_after();
             const uint32_t s0 = smem_u32(stages + stage * STAGE_BYTES);
-  #pragma unroll
+#pragma unroll
             for (int kk = 0; kk < 4; ++kk) {  // 16 of the stage's 64 K values per MMA
               uint64_t adesc, bdesc;
               if (quad) {  // A = E_b K-block, B = the quad's halves' C rows (64 per half, rows of 128 bytes)
